@@ -18,7 +18,9 @@ from ._abi import (MK_MODEL_MOE_LAYER, MK_MODEL_MOE_DECODER, mk_moe_weights, mk_
                    MK_DEBUG_EMPTY_TASKS,
                    MK_SIM_FAULT_NONE, MK_SIM_FAULT_DROP_NOTIFY, MK_SIM_FAULT_COUNT_PLUS_ONE,
                    MK_SIM_FAULT_NO_WAIT, MK_SIM_FAULT_COUNT_MINUS_ONE, OP_NAMES, mk_model_desc, mk_plan_opts, mk_step_args,
-                   mk_layer_weights, mk_device_status, mk_family_info, mk_sim_report)
+                   mk_layer_weights, mk_device_status, mk_family_info, mk_sim_report,
+                   MK_DTYPE_BF16, MK_DTYPE_FP16, MK_DTYPE_FP32, MK_PAGED_ATTN_MAX_BATCH, mk_kv_pages, mk_append_args,
+                   mk_prompt_args, mk_paged_attn_args, mk_logits_args)
 
 _lib = None
 
@@ -144,6 +146,26 @@ def mk_plan_step_bytes(plan: int, batch: int, ctx_lens, with_logits: bool = Fals
 
 def mk_plan_destroy(plan: int):
     lib().mk_plan_destroy(plan)
+
+
+def mk_append_kv(args: mk_append_args, stream: int = 0):
+    _check(lib().mk_append_kv(C.byref(args), stream))
+
+
+def mk_prompt_attention(args: mk_prompt_args, stream: int = 0):
+    _check(lib().mk_prompt_attention(C.byref(args), stream))
+
+
+def mk_paged_attention_workspace_bytes(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().mk_paged_attention_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim))
+
+
+def mk_paged_attention(args: mk_paged_attn_args, stream: int = 0):
+    _check(lib().mk_paged_attention(C.byref(args), stream))
+
+
+def mk_process_logits(args: mk_logits_args, stream: int = 0):
+    _check(lib().mk_process_logits(C.byref(args), stream))
 
 
 # ---------------------------------------------------------------- convenience holder
@@ -344,3 +366,275 @@ class MoELayer:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- serving operators on tensors
+def _refuse(what):
+    raise MkError(MK_ERR_INVALID_ARG, what)
+
+
+def _dtypes():
+    import torch
+    return {torch.bfloat16: MK_DTYPE_BF16, torch.float16: MK_DTYPE_FP16, torch.float32: MK_DTYPE_FP32}
+
+
+def _on(device, **tensors):
+    """Every given tensor is on ``device`` (a CUDA device)."""
+    if device.type != "cuda":
+        _refuse("the tensors must be on a CUDA device")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            _refuse(f"{name} is on {t.device}, not on {device}")
+
+
+def _rows(name, t, shape, dtype):
+    """Strides (row, head) of a [rows][heads][head_dim] tensor whose last dimension is dense."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        _refuse(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        _refuse(f"{name}: the last dimension must be dense")
+    # (the stride of a dimension of size 1 is not used)
+    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _array(name, t, dtype, *shape):
+    """A dense array of exactly this shape (None: not given)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        _refuse(f"{name} must be a dense {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return _ptr(t)
+
+
+def _pages(k, v, page_table, batch):
+    """mk_kv_pages of k, v [n_pages][n_kv_heads][page_size][head_dim] and page_table int32 [batch][width]."""
+    import torch
+    if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+        _refuse("k and v pages must both be bf16 or fp16 [n_pages][n_kv_heads][page_size][head_dim]")
+    used = [i for i in range(3) if k.shape[i] > 1]
+    if (k.shape[3] > 1 and (k.stride(3) != 1 or v.stride(3) != 1)) or any(k.stride(i) != v.stride(i) for i in used):
+        _refuse("k and v pages must have the same strides and a dense last dimension")
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch or
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        _refuse("page_table must be int32 [batch][width] with dense rows")
+    p = mk_kv_pages()
+    p.k, p.v, p.dtype = _ptr(k), _ptr(v), _dtypes()[k.dtype]
+    p.n_pages, p.n_kv_heads, p.page_size, p.head_dim = k.shape
+    p.page_stride, p.head_stride, p.row_stride = (k.stride(i) if i in used else 0 for i in range(3))
+    p.page_table, p.table_width = _ptr(page_table), page_table.shape[1]
+    p.table_stride = page_table.stride(0) if batch > 1 else page_table.shape[1]
+    return p
+
+
+class _launch_on:
+    """The stream a call goes to (``stream``, or the device's current one) with its device current."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is not None and stream.device != device:
+            _refuse(f"the stream is on {stream.device}, the tensors on {device}")
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        self._scope = torch.cuda.stream(self.stream)  # makes the stream's device current too
+
+    def __enter__(self):
+        self._scope.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self._scope.__exit__(*exc)
+
+
+def append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_theta=10000.0, q_out=None, status=None,
+              stream=None):
+    """Turn new tokens' queries and keys to their positions and store keys and values in the cache (mk_append_kv).
+
+    q [T][Hq][D] (or None), k and v [T][Hkv][D] are the packed rows of all sequences (views of one projection's
+    output do), ``cu_seqlens`` int32 [B + 1] their bounds and ``ctx_lens`` int32 [B] the tokens already cached.
+    ``k_pages``/``v_pages`` are [n_pages][Hkv][page_size][D] in any order of the first three dimensions, ``page_table``
+    int32 [B][width]; one layer of a DenseDecoder's cache is such a pool, its slot ids [B][1] the table.
+    ``rope_theta`` 0 (or None) stores the rows unturned.  Returns the turned queries: ``q_out`` (``q`` itself is
+    allowed), or a new tensor, whose rows behind the last sequence are not written.  ``status``: int32 [1],
+    see include/mk.h."""
+    import torch
+    if k.dim() != 3:
+        _refuse("k must be [tokens][n_kv_heads][head_dim]")
+    batch = ctx_lens.numel()
+    _on(k.device, q=q, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, ctx_lens=ctx_lens,
+        cu_seqlens=cu_seqlens, q_out=q_out, status=status)
+    a = mk_append_args()
+    a.pages = _pages(k_pages, v_pages, page_table, batch)
+    T, hkv, D = k.shape
+    a.batch, a.n_tokens = batch, T
+    a.k_row_stride, a.k_head_stride = _rows("k", k, (T, k_pages.shape[1], k_pages.shape[3]), k_pages.dtype)
+    a.v_row_stride, a.v_head_stride = _rows("v", v, k.shape, k.dtype)
+    a.k, a.v = _ptr(k), _ptr(v)
+    a.ctx_lens = _array("ctx_lens", ctx_lens, torch.int32, batch)
+    a.cu_seqlens = _array("cu_seqlens", cu_seqlens, torch.int32, batch + 1)
+    a.status = _array("status", status, torch.int32, 1)
+    a.rope_theta = float(rope_theta or 0.0)
+    with _launch_on(k.device, stream) as s:
+        if q is not None:
+            if q.dim() != 3:
+                _refuse("q must be [tokens][n_q_heads][head_dim]")
+            a.q_row_stride, a.q_head_stride = _rows("q", q, (T, q.shape[1], D), k.dtype)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            a.qo_row_stride, a.qo_head_stride = _rows("q_out", q_out, q.shape, q.dtype)
+            a.n_q_heads, a.q, a.q_out = q.shape[1], _ptr(q), _ptr(q_out)
+        elif q_out is not None:
+            _refuse("q_out without q")
+        mk_append_kv(a, s)
+    return q_out
+
+
+def prompt_attention(q, k, v, cu_q, cu_k=None, page_table=None, kv_lens=None, causal=True, scale=None, out=None,
+                     status=None, stream=None):
+    """Attention over whole prompts, packed one after the other (mk_prompt_attention).
+
+    q [T][Hq][D]; sequence b's queries are rows cu_q[b] .. cu_q[b + 1].  Without ``page_table``, k and v are
+    [Tk][Hkv][D] with bounds ``cu_k`` (default ``cu_q``); with it they are cache pages as in :func:`append_kv` and
+    ``kv_lens`` int32 [B] counts each sequence's keys, the new tokens' own among them.  Causal: the last query of a
+    sequence sees all its keys, each one before it one less.  ``scale`` defaults to 1 / sqrt(D).  Returns ``out``, or
+    a new tensor, whose rows behind the last sequence are not written."""
+    import torch
+    if q.dim() != 3:
+        _refuse("q must be [tokens][n_q_heads][head_dim]")
+    batch = cu_q.numel() - 1
+    _on(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k, page_table=page_table, kv_lens=kv_lens, out=out, status=status)
+    a = mk_prompt_args()
+    if page_table is not None:
+        if kv_lens is None or cu_k is not None:
+            _refuse("paged keys take kv_lens, not cu_k")
+        if page_table.numel() == 0 and batch > 0:
+            _refuse("page_table names no pages")
+        a.pages = _pages(k, v, page_table, batch)
+        a.kv_lens = _array("kv_lens", kv_lens, torch.int32, batch)
+    else:
+        if kv_lens is not None:
+            _refuse("packed keys take cu_k, not kv_lens")
+        if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+            _refuse("k and v must both be bf16 or fp16 [tokens][n_kv_heads][head_dim]")
+        p = a.pages
+        p.row_stride, p.head_stride = _rows("k", k, k.shape, k.dtype)
+        if _rows("v", v, k.shape, k.dtype) != (p.row_stride, p.head_stride):
+            _refuse("k and v must have the same strides")
+        p.k, p.v, p.dtype, p.n_pages = _ptr(k), _ptr(v), _dtypes()[k.dtype], 1
+        p.page_size, p.n_kv_heads, p.head_dim = k.shape
+        a.cu_k = _array("cu_k", cu_q if cu_k is None else cu_k, torch.int32, batch + 1)
+    T, hq, D = q.shape
+    a.batch, a.n_tokens, a.n_q_heads, a.causal, a.scale = batch, T, hq, int(bool(causal)), _scale(scale)
+    a.q_row_stride, a.q_head_stride = _rows("q", q, (T, hq, a.pages.head_dim), k.dtype)
+    a.q = _ptr(q)
+    a.cu_q = _array("cu_q", cu_q, torch.int32, batch + 1)
+    a.status = _array("status", status, torch.int32, 1)
+    with _launch_on(q.device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        a.o_row_stride, a.o_head_stride = _rows("out", out, q.shape, q.dtype)
+        a.out = _ptr(out)
+        mk_prompt_attention(a, s)
+    return out
+
+
+def paged_attention(q, k_pages, v_pages, page_table, kv_lens, scale=None, out=None, workspace=None, status=None,
+                    stream=None):
+    """Attention of one new token per sequence over its cached keys (mk_paged_attention).
+
+    q [B][Hq][D]; pages and ``page_table`` as in :func:`append_kv`; ``kv_lens`` int32 [B] counts each sequence's keys,
+    the new token's own among them (0: a zero row).  ``workspace``: uint8, mk_paged_attention_workspace_bytes long and
+    256-byte aligned (a torch allocation is), not to be shared by calls that overlap; by default one is allocated.
+    Returns ``out`` [B][Hq][D], or a new tensor."""
+    import torch
+    if q.dim() != 3:
+        _refuse("q must be [batch][n_q_heads][head_dim]")
+    B, hq, D = q.shape
+    _on(q.device, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens, out=out,
+        workspace=workspace, status=status)
+    a = mk_paged_attn_args()
+    a.pages = _pages(k_pages, v_pages, page_table, B)
+    a.batch, a.n_q_heads, a.scale = B, hq, _scale(scale)
+    a.q_row_stride, a.q_head_stride = _rows("q", q, (B, hq, k_pages.shape[3]), k_pages.dtype)
+    a.q = _ptr(q)
+    a.kv_lens = _array("kv_lens", kv_lens, torch.int32, B)
+    a.status = _array("status", status, torch.int32, 1)
+    with _launch_on(q.device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(mk_paged_attention_workspace_bytes(B, hq, k_pages.shape[1], D), dtype=torch.uint8,
+                                    device=q.device)
+        a.o_row_stride, a.o_head_stride = _rows("out", out, q.shape, q.dtype)
+        a.out = _ptr(out)
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            _refuse("workspace must be a dense uint8 tensor")
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+        mk_paged_attention(a, s)
+    return out
+
+
+def _scale(scale):
+    """The C ABI's scale: 0 stands for the default."""
+    if scale is None:
+        return 0.0
+    if not float(scale) > 0.0:
+        _refuse("scale must be above 0")
+    return float(scale)
+
+
+def process_logits(logits, history=None, history_lens=None, prompt_lens=None, repetition=None, frequency=None,
+                   presence=None, bias=None, mask=None, out=None, next_tokens=None, status=None, stream=None):
+    """Penalties for repeated tokens, biases and a grammar's mask on logits, and the choice (mk_process_logits).
+
+    logits fp32, bf16 or fp16 [rows][vocab]; ``history`` int32 [rows][n], its rows used up to ``history_lens`` int32
+    [rows], the answer from ``prompt_lens`` on; ``repetition``, ``frequency``, ``presence`` fp32 [rows]; ``bias``
+    (indptr int32 [rows + 1], ids int32 [n], values fp32 [n]); ``mask`` int32 [rows or 1][(vocab + 31) // 32] with a
+    bit set for each allowed id.  Returns (out fp32 [rows][vocab], next_tokens int32 [rows]): the given tensors, or new
+    ones; ``out`` may be ``logits`` itself.  A row in which nothing is left gets token -1."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in _dtypes() or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        _refuse("logits must be fp32, bf16 or fp16 [rows][vocab] with dense rows")
+    R, V = logits.shape
+    a = mk_logits_args()
+    a.rows, a.vocab, a.dtype, a.logits = R, V, _dtypes()[logits.dtype], _ptr(logits)
+    a.logits_stride = logits.stride(0) if R > 1 else V
+    indptr, ids, values = bias if bias is not None else (None, None, None)
+    _on(logits.device, history=history, history_lens=history_lens, prompt_lens=prompt_lens, repetition=repetition,
+        frequency=frequency, presence=presence, indptr=indptr, ids=ids, values=values, mask=mask, out=out,
+        next_tokens=next_tokens, status=status)
+    if history is not None:
+        if (history.dtype != torch.int32 or history.dim() != 2 or history.shape[0] != R or
+                (history.shape[1] > 1 and history.stride(1) != 1)):
+            _refuse("history must be int32 [rows][n] with dense rows")
+        a.history_width = history.shape[1]
+        a.history_stride = history.stride(0) if R > 1 else history.shape[1]
+        a.history = _ptr(history) if history.shape[1] else 0
+    if a.history:
+        a.history_lens = _array("history_lens", history_lens, torch.int32, R)
+        a.prompt_lens = _array("prompt_lens", prompt_lens, torch.int32, R)
+        a.repetition = _array("repetition", repetition, torch.float32, R)
+        a.frequency = _array("frequency", frequency, torch.float32, R)
+        a.presence = _array("presence", presence, torch.float32, R)
+    elif history is None and any(t is not None for t in (history_lens, prompt_lens, repetition, frequency, presence)):
+        _refuse("penalties and history lengths need a history")
+    if bias is not None and ids.numel():
+        a.bias_count = ids.numel()
+        a.bias_indptr = _array("bias indptr", indptr, torch.int32, R + 1)
+        a.bias_ids = _array("bias ids", ids, torch.int32, a.bias_count)
+        a.bias_values = _array("bias values", values, torch.float32, a.bias_count)
+    if mask is not None:
+        if (mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[0] not in (1, R) or
+                mask.shape[1] != (V + 31) // 32 or (mask.shape[1] > 1 and mask.stride(1) != 1)):
+            _refuse("mask must be int32 [rows or 1][(vocab + 31) // 32] with dense rows")
+        a.mask, a.mask_stride = _ptr(mask), mask.stride(0) if mask.shape[0] > 1 else 0
+    a.status = _array("status", status, torch.int32, 1)
+    with _launch_on(logits.device, stream) as s:
+        if out is None:
+            out = torch.empty((R, V), dtype=torch.float32, device=logits.device)
+        if next_tokens is None:
+            next_tokens = torch.empty(R, dtype=torch.int32, device=logits.device)
+        if out.dtype != torch.float32 or out.shape != logits.shape or (V > 1 and out.stride(1) != 1):
+            _refuse("out must be fp32 [rows][vocab] with dense rows")
+        a.out, a.out_stride = _ptr(out), out.stride(0) if R > 1 else V
+        a.next_tokens = _array("next_tokens", next_tokens, torch.int32, R)
+        mk_process_logits(a, s)
+    return out, next_tokens

@@ -25,6 +25,11 @@ MK_DEBUG_TRACE = 2
 MK_DEBUG_EMPTY_TASKS = 4
 MK_STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 
+MK_DTYPE_BF16 = 0
+MK_DTYPE_FP16 = 1
+MK_DTYPE_FP32 = 2
+MK_PAGED_ATTN_MAX_BATCH = 4096
+
 MK_SIM_FAULT_NONE = 0
 MK_SIM_FAULT_DROP_NOTIFY = 1
 MK_SIM_FAULT_COUNT_PLUS_ONE = 2
@@ -90,6 +95,56 @@ class mk_step_args(C.Structure):
     ]
 
 
+class mk_kv_pages(C.Structure):
+    _fields_ = [
+        ("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+        ("n_pages", C.c_int), ("page_size", C.c_int), ("page_stride", C.c_longlong), ("head_stride", C.c_longlong),
+        ("row_stride", C.c_longlong), ("page_table", C.c_void_p), ("table_width", C.c_int), ("table_stride", C.c_int),
+    ]
+
+
+class mk_append_args(C.Structure):
+    _fields_ = [
+        ("pages", mk_kv_pages), ("batch", C.c_int), ("n_tokens", C.c_int), ("n_q_heads", C.c_int),
+        ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_out", C.c_void_p),
+        ("q_row_stride", C.c_longlong), ("q_head_stride", C.c_longlong), ("k_row_stride", C.c_longlong),
+        ("k_head_stride", C.c_longlong), ("v_row_stride", C.c_longlong), ("v_head_stride", C.c_longlong),
+        ("qo_row_stride", C.c_longlong), ("qo_head_stride", C.c_longlong),
+        ("cu_seqlens", C.c_void_p), ("ctx_lens", C.c_void_p), ("rope_theta", C.c_double), ("status", C.c_void_p),
+    ]
+
+
+class mk_prompt_args(C.Structure):
+    _fields_ = [
+        ("pages", mk_kv_pages), ("batch", C.c_int), ("n_tokens", C.c_int), ("n_q_heads", C.c_int),
+        ("causal", C.c_int), ("scale", C.c_float), ("q", C.c_void_p), ("out", C.c_void_p),
+        ("q_row_stride", C.c_longlong), ("q_head_stride", C.c_longlong), ("o_row_stride", C.c_longlong),
+        ("o_head_stride", C.c_longlong), ("cu_q", C.c_void_p), ("cu_k", C.c_void_p), ("kv_lens", C.c_void_p),
+        ("status", C.c_void_p),
+    ]
+
+
+class mk_paged_attn_args(C.Structure):
+    _fields_ = [
+        ("pages", mk_kv_pages), ("batch", C.c_int), ("n_q_heads", C.c_int), ("scale", C.c_float),
+        ("q", C.c_void_p), ("out", C.c_void_p), ("q_row_stride", C.c_longlong), ("q_head_stride", C.c_longlong),
+        ("o_row_stride", C.c_longlong), ("o_head_stride", C.c_longlong), ("kv_lens", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t), ("status", C.c_void_p),
+    ]
+
+
+class mk_logits_args(C.Structure):
+    _fields_ = [
+        ("rows", C.c_int), ("vocab", C.c_int), ("dtype", C.c_int), ("logits", C.c_void_p),
+        ("logits_stride", C.c_longlong), ("out", C.c_void_p), ("out_stride", C.c_longlong),
+        ("next_tokens", C.c_void_p), ("history", C.c_void_p), ("history_width", C.c_int),
+        ("history_stride", C.c_longlong), ("history_lens", C.c_void_p), ("prompt_lens", C.c_void_p),
+        ("repetition", C.c_void_p), ("frequency", C.c_void_p), ("presence", C.c_void_p),
+        ("bias_indptr", C.c_void_p), ("bias_ids", C.c_void_p), ("bias_values", C.c_void_p), ("bias_count", C.c_int),
+        ("mask", C.c_void_p), ("mask_stride", C.c_longlong), ("status", C.c_void_p),
+    ]
+
+
 class mk_device_status(C.Structure):
     _fields_ = [("code", C.c_int), ("family", C.c_int), ("index", C.c_int), ("event", C.c_int), ("sm", C.c_int)]
 
@@ -134,6 +189,11 @@ PROTOTYPES = {
                                    C.c_int, C.POINTER(mk_sim_report)]),
     "mk_plan_step_bytes": (C.c_double, [C.c_void_p, C.c_int, C.POINTER(C.c_int), C.c_int]),
     "mk_plan_destroy": (None, [C.c_void_p]),
+    "mk_append_kv": (C.c_int, [C.POINTER(mk_append_args), C.c_void_p]),
+    "mk_prompt_attention": (C.c_int, [C.POINTER(mk_prompt_args), C.c_void_p]),
+    "mk_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
+    "mk_paged_attention": (C.c_int, [C.POINTER(mk_paged_attn_args), C.c_void_p]),
+    "mk_process_logits": (C.c_int, [C.POINTER(mk_logits_args), C.c_void_p]),
 }
 
 

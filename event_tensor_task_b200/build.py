@@ -1,39 +1,40 @@
 """Build libmk.so in-tree with nvcc for sm_100a (B200).
 
-``python -m event_tensor_task_b200.build`` or ``build()`` from Python.  The
-library is rebuilt when any source under ``csrc/`` or ``include/`` is newer
-than it.
+``python -m event_tensor_task_b200.build`` or ``build()`` from Python.  A
+source is compiled again when it, or any header under ``csrc/`` or
+``include/``, is newer than its object (kept under ``_build/``); the sources
+compile side by side.
 """
 import glob
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmk.so")
+OBJ = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
-SOURCES = ["csrc/megakernel.cu", "csrc/plan.cpp", "csrc/api.cpp"]
+SOURCES = ["csrc/megakernel.cu", "csrc/plan.cpp", "csrc/api.cpp", "csrc/serve_checks.cpp", "csrc/append_kv.cu",
+           "csrc/prompt_attn.cu", "csrc/paged_attn.cu", "csrc/logits.cu"]
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-shared", "-lcudart",
-    "--expt-relaxed-constexpr",
+    "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr",
 ]
 
 
+def _newer(path, than) -> bool:
+    return not os.path.exists(than) or os.path.getmtime(path) > os.path.getmtime(than)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
     deps = glob.glob(os.path.join(HERE, "csrc", "*")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return any(_newer(d, LIB) for d in deps + [os.path.join(HERE, "build.py")])
 
 
-def build(force: bool = False, verbose: bool = False, extra=None) -> str:
-    if not force and not _stale():
-        return LIB
-    cmd = [NVCC] + FLAGS + (extra or []) + ["-o", LIB] + [os.path.join(HERE, s) for s in SOURCES]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, cwd=HERE, capture_output=True, text=True)
@@ -41,6 +42,24 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
     if verbose and (r.stdout or r.stderr):
         print(r.stdout + r.stderr)
+
+
+def build(force: bool = False, verbose: bool = False, extra=None) -> str:
+    if not force and not _stale():
+        return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    headers = [os.path.join(HERE, "build.py")] + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    for ext in ("*.h", "*.hpp", "*.cuh"):
+        headers += glob.glob(os.path.join(HERE, "csrc", ext))
+    todo, objects = [], []
+    for s in SOURCES:
+        src, obj = os.path.join(HERE, s), os.path.join(OBJ, os.path.basename(s) + ".o")
+        objects.append(obj)
+        if force or any(_newer(d, obj) for d in [src] + headers):
+            todo.append([NVCC] + FLAGS + (extra or []) + ["-c", "-o", obj, src])
+    with ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), todo))
+    _run([NVCC] + FLAGS + ["-shared", "-lcudart", "-o", LIB] + objects, verbose)
     return LIB
 
 

@@ -13,6 +13,7 @@
 #include "../../include/mk.h"
 #include "launch.hpp"
 #include "plan.hpp"
+#include "serve.hpp"
 
 struct mk_plan {
   mk::Plan p;
@@ -37,6 +38,23 @@ bool binding_from(const mk_plan* hp, int batch, const int* ctx, mk::Binding& bd)
   if (batch > hp->p.dp.max_batch || !ctx) return false;
   bd.ctx.assign(ctx, ctx + batch);
   return true;
+}
+
+// A serving operator: nothing to do without rows; else checks the arguments and enqueues.
+template <class Args>
+mk_status serve(const Args* a, bool (*empty)(const Args&), mk_status (*check)(const Args&, std::string&),
+                mk_status (*launch)(const Args&, void*, std::string&), void* stream) {
+  g_err.clear();
+  if (!a) return fail(MK_ERR_INVALID_ARG, "null argument");
+  try {
+    std::string err;
+    if (empty(*a)) return MK_OK;  // (an empty array may have no address)
+    mk_status s = check(*a, err);
+    if (s == MK_OK) s = launch(*a, stream, err);
+    return s == MK_OK ? MK_OK : fail(s, err);
+  } catch (...) {
+    return fail(MK_ERR_CUDA, "unexpected error in a serving operator");
+  }
 }
 }  // namespace
 
@@ -278,5 +296,29 @@ double mk_plan_step_bytes(const mk_plan* hp, int batch, const int* ctx, int with
 }
 
 void mk_plan_destroy(mk_plan* hp) { delete hp; }
+
+mk_status mk_append_kv(const mk_append_args* a, void* stream) {
+  return serve<mk_append_args>(a, [](const mk_append_args& x) { return x.batch == 0 || x.n_tokens == 0; },
+                               mk::check_append, mk::launch_append, stream);
+}
+
+mk_status mk_prompt_attention(const mk_prompt_args* a, void* stream) {
+  return serve<mk_prompt_args>(a, [](const mk_prompt_args& x) { return x.batch == 0 || x.n_tokens == 0; },
+                               mk::check_prompt, mk::launch_prompt, stream);
+}
+
+size_t mk_paged_attention_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim) {
+  return mk::paged_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim);
+}
+
+mk_status mk_paged_attention(const mk_paged_attn_args* a, void* stream) {
+  return serve<mk_paged_attn_args>(a, [](const mk_paged_attn_args& x) { return x.batch == 0; }, mk::check_paged,
+                                   mk::launch_paged, stream);
+}
+
+mk_status mk_process_logits(const mk_logits_args* a, void* stream) {
+  return serve<mk_logits_args>(a, [](const mk_logits_args& x) { return x.rows == 0; }, mk::check_logits,
+                               mk::launch_logits, stream);
+}
 
 }  // extern "C"

@@ -1,0 +1,136 @@
+// append_kv.cu — mk_append_kv: new tokens' query and key rows turned to their
+// positions, key and value rows stored in the cache's pages.
+//
+// Mathematics: pair (x, y) = (row[p], row[p + D/2]) of every query and key
+// head becomes (x cos a - y sin a, y cos a + x sin a), a = position *
+// theta^(-2p/D).  The frequency and the product are taken in double, since a
+// far position times a frequency loses its fraction in fp32; the angle is
+// brought into [-pi, pi] in double and only then handed to the fp32 sine and
+// cosine.  One angle serves all heads of a token, so a block computes its
+// tokens' angles once into shared memory and the heads read them there.
+//
+// Bound: memory.  Every row is read and written once, 16 bytes a thread and
+// access; a thread turns 8 pairs (a 16-byte piece of each half of a head).
+#include <cmath>
+
+#include "serve.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;  // tokens of a block
+
+struct AppendParams {
+  mk_append_args a;
+  double freq[64];  // theta^(-2p/D)
+};
+
+template <class T, int D, int TOK>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams P) {
+  constexpr int H = D / 2, PIECES = D / 16;  // pairs of a head; 16-byte pieces of half a head
+  const mk_append_args& a = P.a;
+  __shared__ float2 turn[TOK][H];          // (cos, sin)
+  __shared__ long long dest[TOK];          // first element of the token's row in head 0 of its page, or -1
+  __shared__ int where[TOK];               // position, or -1: row behind the last sequence
+  const int t0 = blockIdx.x * TOK;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // a warp per token: its sequence is the number of sequences that end at or before it
+  if (warp < TOK) {
+    const int t = t0 + warp;
+    int n = 0;
+    for (int b = lane; b < a.batch; b += 32) n += __ldg(a.cu_seqlens + b + 1) <= t;
+    n = __reduce_add_sync(~0u, n);
+    if (lane == 0) {
+      int pos = -1;
+      long long d = -1;
+      if (t < a.n_tokens && n < a.batch) {
+        const int begin = __ldg(a.cu_seqlens + n), ctx = __ldg(a.ctx_lens + n);
+        const long long at = (long long)ctx + t - begin;
+        if (begin < 0 || begin > t || ctx < 0 || at >= (long long)a.pages.table_width * a.pages.page_size) {
+          if (begin <= t) report_bounds(a.status);  // (begin > t: a row before the first sequence)
+        } else {
+          const int page = page_of(a.pages, n, (int)(at / a.pages.page_size), a.status);
+          if (page >= 0) {
+            pos = (int)at;
+            d = (long long)page * a.pages.page_stride + (at % a.pages.page_size) * a.pages.row_stride;
+          }
+        }
+      }
+      where[warp] = pos;
+      dest[warp] = d;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < TOK * H; i += kThreads) {
+    const int tok = i / H, p = i % H;
+    float2 cs = make_float2(1.f, 0.f);
+    if (where[tok] > 0 && a.rope_theta != 0.0) {
+      const double angle = (double)where[tok] * P.freq[p];
+      const double turns = rint(angle * 0.15915494309189535);  // 1 / (2 pi)
+      const float r = (float)fma(turns, -6.283185307179586, angle);
+      sincosf(r, &cs.y, &cs.x);
+    }
+    turn[tok][p] = cs;
+  }
+  __syncthreads();
+
+  const int hq = a.q ? a.n_q_heads : 0, hkv = a.pages.n_kv_heads;
+  const int per_token = (hq + 2 * hkv) * PIECES;
+  for (int i = threadIdx.x; i < TOK * per_token; i += kThreads) {
+    const int tok = i / per_token, r = i % per_token, head = r / PIECES, c = (r % PIECES) * 8;
+    if (dest[tok] < 0) continue;
+    const long long t = t0 + tok;
+    const T* src;
+    T* dst;
+    if (head < hq) {
+      src = static_cast<const T*>(a.q) + t * a.q_row_stride + head * a.q_head_stride;
+      dst = static_cast<T*>(a.q_out) + t * a.qo_row_stride + head * a.qo_head_stride;
+    } else if (head < hq + hkv) {
+      const int h = head - hq;
+      src = static_cast<const T*>(a.k) + t * a.k_row_stride + h * a.k_head_stride;
+      dst = static_cast<T*>(a.pages.k) + dest[tok] + h * a.pages.head_stride;
+    } else {
+      const int h = head - hq - hkv;
+      src = static_cast<const T*>(a.v) + t * a.v_row_stride + h * a.v_head_stride;
+      dst = static_cast<T*>(a.pages.v) + dest[tok] + h * a.pages.head_stride;
+    }
+    uint4 lo = *reinterpret_cast<const uint4*>(src + c), hi = *reinterpret_cast<const uint4*>(src + c + H);
+    if (head < hq + hkv && a.rope_theta != 0.0) {
+      uint32_t* l = &lo.x;
+      uint32_t* h = &hi.x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = Elem<T>::unpack(l[j]), y = Elem<T>::unpack(h[j]);
+        const float2 u = turn[tok][c + 2 * j], w = turn[tok][c + 2 * j + 1];
+        l[j] = Elem<T>::pack(x.x * u.x - y.x * u.y, x.y * w.x - y.y * w.y);
+        h[j] = Elem<T>::pack(y.x * u.x + x.x * u.y, y.y * w.x + x.y * w.y);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + c) = lo;
+    *reinterpret_cast<uint4*>(dst + c + H) = hi;
+  }
+}
+
+template <class T, int D>
+mk_status launch(const AppendParams& P, cudaStream_t s, std::string& err) {
+  const int n = P.a.n_tokens;
+  append_kernel<T, D, kMaxTokens><<<(n + kMaxTokens - 1) / kMaxTokens, kThreads, 0, s>>>(P);
+  return cuda_result(cudaGetLastError(), "mk_append_kv launch", err);
+}
+
+}  // namespace
+
+mk_status launch_append(const mk_append_args& a, void* stream, std::string& err) {
+  AppendParams P;
+  P.a = a;
+  const int D = a.pages.head_dim;
+  for (int p = 0; p < 64; ++p) P.freq[p] = a.rope_theta != 0.0 && p < D / 2 ? std::pow(a.rope_theta, -2.0 * p / D) : 0.0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.pages.dtype == MK_DTYPE_BF16)
+    return D == 64 ? launch<__nv_bfloat16, 64>(P, s, err) : launch<__nv_bfloat16, 128>(P, s, err);
+  return D == 64 ? launch<__half, 64>(P, s, err) : launch<__half, 128>(P, s, err);
+}
+
+}  // namespace mk

@@ -1,0 +1,531 @@
+// paged_attn.cu — mk_paged_attention: attention of one new token per sequence
+// over its cached keys, in pages.
+//
+// Mathematics: out = sum_j p_j v_j / sum_j p_j with p_j = 2^(c (q.k_j) - m),
+// c = scale log2 e, m a running maximum: one pass over keys and values, parts
+// with their own (m, l = sum p, O = sum p v) joined exactly as in the loop.
+//
+// Bound: memory; every cached row is read once, G = n_q_heads / n_kv_heads
+// query heads share it.  So:
+//  - the keys of all (sequence, kv head) pairs are laid end to end in units of
+//    64 and cut into equal shares, one per resident block, whatever the
+//    sequences' lengths; a block's share begins and ends inside a pair, so it
+//    leaves at most two partial results, and a second kernel joins them;
+//  - a warp owns 16 keys of each unit and runs alone: its own ring of stages
+//    in shared memory (cp.async, 16 bytes a lane, rows gathered through the
+//    page table, zeros past the end), its own running maximum, sum and output
+//    in registers; the block's four warps meet only where a pair ends;
+//  - the products are warp MMAs (m16n8k16, the group's heads as rows): at most
+//    16 rows make a tile too small for tcgen05, whose M is 64 or more, and the
+//    tensor pipe is nearly idle either way.  With G <= 8 the spare rows carry
+//    what rounding takes off the probabilities (value and remainder), above 8
+//    the remainders take a second MMA: the sum sees ~16 bits of p.
+#include <cmath>
+
+#include "serve.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kThreads = 128, kWarps = 4;
+constexpr int kKeys = 16;               // keys of a warp's piece of a unit
+constexpr int kUnit = kKeys * kWarps;   // keys of a unit
+constexpr int kRows = 16;               // query heads of a tile
+constexpr int kMaxCtas = 640;           // the workspace holds two partials of each
+
+template <int D>
+struct Shape {
+  static constexpr int kPiece = kKeys * D * 2 * 2;  // bytes of a warp's keys and values
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kBlocksPerSm = 2;
+  static constexpr int kMerge = 2 * kRows * D * 4;  // two output tiles in fp32
+  static constexpr int kSmem = kWarps * kStages * kPiece + kMerge;
+  static constexpr int kPartial = 2 * kRows + kRows * D;  // floats: m, l, O
+};
+
+struct PagedParams {
+  mk_paged_attn_args a;
+  float scale_log2;
+  int group, tiles;    // G; tiles of 16 heads per kv head
+  int n_cta;
+  float* partial;      // [n_cta][2][kPartial]
+};
+
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 bytes global -> shared, zeros where !live
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// keys of sequence b that are there to see
+__device__ __forceinline__ int keys_of(const mk_paged_attn_args& a, int b) {
+  const int n = __ldg(a.kv_lens + b), cap = a.pages.table_width * a.pages.page_size;
+  if (n < 0 || n > cap) {
+    report_bounds(a.status);
+    return n < 0 ? 0 : cap;
+  }
+  return n;
+}
+
+// The units of all sequences end to end, and where unit `u` or sequence `b` lies among them.
+// Called by the whole block of NT threads; `scratch` holds NT + 1 sums.
+struct Layout {
+  long long total;
+  long long before;  // units before the sequence asked for
+  int b;
+};
+template <int NT>
+__device__ __forceinline__ long long scan_units(const PagedParams& P, long long* scratch, int& per) {
+  const int B = P.a.batch, pairs = P.a.pages.n_kv_heads * P.tiles;
+  per = (B + NT - 1) / NT;
+  long long mine = 0;
+  for (int b = threadIdx.x * per; b < min(B, (int)(threadIdx.x + 1) * per); ++b)
+    mine += (long long)((keys_of(P.a, b) + kUnit - 1) / kUnit) * pairs;
+  // exclusive sums over the block
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long sum = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(~0u, sum, d);
+    if (lane >= d) sum += o;
+  }
+  __shared__ long long warp_sum[NT / 32];
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  long long base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) base += warp_sum[w];
+    total += warp_sum[w];
+  }
+  scratch[threadIdx.x] = base + sum - mine;
+  if (threadIdx.x == 0) scratch[NT] = total;
+  __syncthreads();
+  return total;
+}
+
+// One pair's place in the flattened order: sequence b, head tile h (kv head * tiles + tile).
+struct Walk {
+  int b, h, tile, ntile, len;
+  __device__ __forceinline__ void enter(const PagedParams& P, int seq) {
+    b = seq;
+    for (;;) {
+      len = b < P.a.batch ? keys_of(P.a, b) : 0;
+      ntile = (len + kUnit - 1) / kUnit;
+      if (ntile > 0 || b >= P.a.batch) break;
+      ++b;
+    }
+    h = tile = 0;
+  }
+  __device__ __forceinline__ void next(const PagedParams& P) {
+    if (++tile < ntile) return;
+    tile = 0;
+    if (++h < P.a.pages.n_kv_heads * P.tiles) return;
+    enter(P, b + 1);
+  }
+};
+
+// first element of key `t` of the pair's rows; -1: no such key (zeros)
+__device__ __forceinline__ long long row_offset(const PagedParams& P, const Walk& w, int t) {
+  if (t >= w.len) return -1;
+  const mk_kv_pages& g = P.a.pages;
+  const unsigned page_index = (unsigned)t / (unsigned)g.page_size, row = (unsigned)t % (unsigned)g.page_size;
+  const int page = page_of(g, w.b, page_index, P.a.status);
+  if (page < 0) return -1;
+  return page * g.page_stride + (long long)(w.h / P.tiles) * g.head_stride + row * g.row_stride;
+}
+
+// FULL: 9 to 16 heads in the tile (both halves of the MMA's rows are heads)
+template <class T, int D, bool FULL>
+__global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel(const __grid_constant__ PagedParams P) {
+  using S = Shape<D>;
+  constexpr int CH = D / 8;  // 16-byte chunks of a row
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long scratch[kThreads + 1];
+  __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int quad = lane >> 2, sub = lane & 3;
+  float* merge = reinterpret_cast<float*>(smem + kWarps * S::kStages * S::kPiece);
+  const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kPiece;
+
+  int per;
+  const long long total = scan_units<kThreads>(P, scratch, per);
+  const long long u0 = total * blockIdx.x / P.n_cta, u1 = total * (blockIdx.x + 1) / P.n_cta;
+  if (u0 >= u1) return;
+
+  Walk load;
+  {
+    // the last group of sequences that begins at or before u0 (all threads alike)
+    int lo = 0, hi = kThreads - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (scratch[mid] <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    long long at = scratch[lo];
+    const int pairs = P.a.pages.n_kv_heads * P.tiles;
+    load.enter(P, lo * per);
+    while (at + (long long)load.ntile * pairs <= u0) {
+      at += (long long)load.ntile * pairs;
+      load.enter(P, load.b + 1);
+    }
+    load.h = (int)((u0 - at) / load.ntile);
+    load.tile = (int)((u0 - at) % load.ntile);
+  }
+  Walk use = load;
+  const int n_units = (int)(u1 - u0);
+
+  // the lane's key of the piece that is loaded next; its offset is looked up one unit ahead
+  const int my_key = warp * kKeys + (lane & 15);
+  long long off = row_offset(P, load, load.tile * kUnit + my_key);
+  const char* kbase = static_cast<const char*>(P.a.pages.k);
+  const char* vbase = static_cast<const char*>(P.a.pages.v);
+  int issued = 0;
+  auto issue = [&]() {
+    if (issued < n_units) {
+      const uint32_t st = ring + (issued % S::kStages) * S::kPiece;
+#pragma unroll
+      for (int i = 0; i < kKeys * CH / 32; ++i) {
+        const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+        const long long o = __shfl_sync(~0u, off, r);
+        const uint32_t d = st + r * (D * 2) + ((c ^ (r & 7)) << 4);
+        const long long byte = (o < 0 ? 0 : o + c * 8) * 2;
+        cp16(d, kbase + byte, o >= 0);
+        cp16(d + kKeys * D * 2, vbase + byte, o >= 0);
+      }
+      ++issued;
+      if (issued < n_units) {
+        load.next(P);
+        off = row_offset(P, load, load.tile * kUnit + my_key);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S::kStages - 1; ++i) issue();
+
+  int slot = 0;  // the partial that the next unfinished pair goes to
+  for (int u = 0; u < n_units;) {
+    // ---- one pair's part: its units in this share
+    const int n_here = min(use.ntile - use.tile, n_units - u);
+    const int first_head = (use.h / P.tiles) * P.group + (use.h % P.tiles) * kRows;
+    const int heads = min(kRows, P.group - (use.h % P.tiles) * kRows);
+    uint32_t q[D / 16][4];
+    {
+      const T* row0 = static_cast<const T*>(P.a.q) + use.b * P.a.q_row_stride + (first_head + quad) * P.a.q_head_stride;
+      const T* row1 = row0 + 8 * P.a.q_head_stride;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][0] = quad < heads ? __ldg(reinterpret_cast<const uint32_t*>(row0 + 16 * k + 2 * sub)) : 0u;
+        q[k][2] = quad < heads ? __ldg(reinterpret_cast<const uint32_t*>(row0 + 16 * k + 8 + 2 * sub)) : 0u;
+        if (FULL) {
+          q[k][1] = quad + 8 < heads ? __ldg(reinterpret_cast<const uint32_t*>(row1 + 16 * k + 2 * sub)) : 0u;
+          q[k][3] = quad + 8 < heads ? __ldg(reinterpret_cast<const uint32_t*>(row1 + 16 * k + 8 + 2 * sub)) : 0u;
+        } else {
+          q[k][1] = q[k][0];
+          q[k][3] = q[k][2];
+        }
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    for (int i = 0; i < n_here; ++i, ++u) {
+      issue();
+      cp_wait<S::kStages - 1>();
+      __syncwarp();
+      const uint32_t kt = ring + (u % S::kStages) * S::kPiece, vt = kt + kKeys * D * 2;
+      float s[2][4] = {};
+      {
+        // matrices: (keys 0-7, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 0-7), (keys 8-15, dims 8-15)
+        const int r = (lane & 7) + ((lane >> 4) << 3), c1 = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          ldsm4(b, kt + r * (D * 2) + (((2 * k + c1) ^ (r & 7)) << 4));
+          mma16816<T>(s[0], q[k], b[0], b[1]);
+          mma16816<T>(s[1], q[k], b[2], b[3]);
+        }
+      }
+      const int left = use.len - (use.tile + i) * kUnit - warp * kKeys;  // keys of the piece that exist
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = t * 8 + 2 * sub + (e & 1);
+          s[t][e] = key < left ? s[t][e] * P.scale_log2 : -INFINITY;
+        }
+      float n0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+      n0 = fmaxf(n0, __shfl_xor_sync(~0u, n0, 1));
+      n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(~0u, n0, 2)));
+      float n1 = n0;
+      if (FULL) {
+        n1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        n1 = fmaxf(n1, __shfl_xor_sync(~0u, n1, 1));
+        n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(~0u, n1, 2)));
+      }
+      if (__any_sync(~0u, n0 > m0 || n1 > m1)) {
+        // a maximum moved: what was summed is brought to it (exp2f(-inf) = 0 at the first piece)
+        const float f0 = n0 > m0 ? exp2f(m0 - n0) : 1.f, f1 = FULL ? (n1 > m1 ? exp2f(m1 - n1) : 1.f) : f0;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          o[k][0] *= f0;
+          o[k][1] *= f0;
+          o[k][2] *= f1;
+          o[k][3] *= f1;
+        }
+        m0 = n0;
+        m1 = n1;
+      }
+      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float p0 = exp2f(s[t][0] - z0), p1 = exp2f(s[t][1] - z0);
+        l0 += p0 + p1;
+        hi[2 * t] = Elem<T>::pack(p0, p1);
+        float2 h = Elem<T>::unpack(hi[2 * t]);
+        const uint32_t rest0 = Elem<T>::pack(p0 - h.x, p1 - h.y);
+        if (FULL) {
+          const float p2 = exp2f(s[t][2] - z1), p3 = exp2f(s[t][3] - z1);
+          l1 += p2 + p3;
+          hi[2 * t + 1] = Elem<T>::pack(p2, p3);
+          h = Elem<T>::unpack(hi[2 * t + 1]);
+          lo[2 * t] = rest0;
+          lo[2 * t + 1] = Elem<T>::pack(p2 - h.x, p3 - h.y);
+        } else {
+          hi[2 * t + 1] = rest0;  // rows 8 to 15: the remainders of rows 0 to 7
+        }
+      }
+      {
+        // transposed: (keys 0-7, dims 0-7), (keys 8-15, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 8-15)
+        const int r = lane & 15, c1 = lane >> 4;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          ldsm4_trans(b, vt + r * (D * 2) + (((2 * k + c1) ^ (r & 7)) << 4));
+          mma16816<T>(o[2 * k], hi, b[0], b[1]);
+          mma16816<T>(o[2 * k + 1], hi, b[2], b[3]);
+          if (FULL) {
+            mma16816<T>(o[2 * k], lo, b[0], b[1]);
+            mma16816<T>(o[2 * k + 1], lo, b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();  // the stage is read before the next copy into it is issued
+    }
+
+    // ---- the four warps' parts meet
+    l0 += __shfl_xor_sync(~0u, l0, 1);
+    l0 += __shfl_xor_sync(~0u, l0, 2);
+    if (FULL) {
+      l1 += __shfl_xor_sync(~0u, l1, 1);
+      l1 += __shfl_xor_sync(~0u, l1, 2);
+    } else {
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        o[k][0] += o[k][2];
+        o[k][1] += o[k][3];
+      }
+    }
+    if (sub == 0) {
+      part_m[warp][quad] = m0;
+      part_l[warp][quad] = l0;
+      if (FULL) {
+        part_m[warp][quad + 8] = m1;
+        part_l[warp][quad + 8] = l1;
+      }
+    }
+    __syncthreads();
+    float top0 = -INFINITY, top1 = -INFINITY, sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      top0 = fmaxf(top0, part_m[w][quad]);
+      if (FULL) top1 = fmaxf(top1, part_m[w][quad + 8]);
+    }
+    // (unit 0 of a part always holds a key, so the tops are finite; a warp without one has weight 0)
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      sum0 += part_l[w][quad] * exp2f(part_m[w][quad] - top0);
+      if (FULL) sum1 += part_l[w][quad + 8] * exp2f(part_m[w][quad + 8] - top1);
+    }
+    const float f0 = exp2f(m0 - top0), f1 = FULL ? exp2f(m1 - top1) : 0.f;
+    float* buf = merge + (warp & 1) * kRows * D;
+    if (warp >= 2) {
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        *reinterpret_cast<float2*>(buf + quad * D + 8 * k + 2 * sub) = make_float2(o[k][0] * f0, o[k][1] * f0);
+        if (FULL)
+          *reinterpret_cast<float2*>(buf + (quad + 8) * D + 8 * k + 2 * sub) = make_float2(o[k][2] * f1, o[k][3] * f1);
+      }
+    }
+    __syncthreads();
+    if (warp < 2) {
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        float2* p = reinterpret_cast<float2*>(buf + quad * D + 8 * k + 2 * sub);
+        o[k][0] = o[k][0] * f0 + p->x;
+        o[k][1] = o[k][1] * f0 + p->y;
+        if (warp == 1) *p = make_float2(o[k][0], o[k][1]);
+        if (FULL) {
+          p = reinterpret_cast<float2*>(buf + (quad + 8) * D + 8 * k + 2 * sub);
+          o[k][2] = o[k][2] * f1 + p->x;
+          o[k][3] = o[k][3] * f1 + p->y;
+          if (warp == 1) *p = make_float2(o[k][2], o[k][3]);
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = n_here == use.ntile;
+    if (warp == 0) {
+      const float* other = merge + kRows * D;
+      if (whole) {
+        const float i0 = 1.f / sum0, i1 = FULL ? 1.f / sum1 : 0.f;
+        T* row0 = static_cast<T*>(P.a.out) + use.b * P.a.o_row_stride + (first_head + quad) * P.a.o_head_stride;
+        T* row1 = row0 + 8 * P.a.o_head_stride;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const float2 p = *reinterpret_cast<const float2*>(other + quad * D + 8 * k + 2 * sub);
+          if (quad < heads)
+            *reinterpret_cast<uint32_t*>(row0 + 8 * k + 2 * sub) = Elem<T>::pack((o[k][0] + p.x) * i0, (o[k][1] + p.y) * i0);
+          if (FULL && quad + 8 < heads) {
+            const float2 r = *reinterpret_cast<const float2*>(other + (quad + 8) * D + 8 * k + 2 * sub);
+            *reinterpret_cast<uint32_t*>(row1 + 8 * k + 2 * sub) = Elem<T>::pack((o[k][2] + r.x) * i1, (o[k][3] + r.y) * i1);
+          }
+        }
+      } else {
+        float* part = P.partial + ((long long)blockIdx.x * 2 + slot) * S::kPartial;
+        if (sub == 0) {
+          part[quad] = top0;
+          part[kRows + quad] = sum0;
+          if (FULL) {
+            part[quad + 8] = top1;
+            part[kRows + quad + 8] = sum1;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const float2 p = *reinterpret_cast<const float2*>(other + quad * D + 8 * k + 2 * sub);
+          *reinterpret_cast<float2*>(part + 2 * kRows + quad * D + 8 * k + 2 * sub) = make_float2(o[k][0] + p.x, o[k][1] + p.y);
+          if (FULL) {
+            const float2 r = *reinterpret_cast<const float2*>(other + (quad + 8) * D + 8 * k + 2 * sub);
+            *reinterpret_cast<float2*>(part + 2 * kRows + (quad + 8) * D + 8 * k + 2 * sub) =
+                make_float2(o[k][2] + r.x, o[k][3] + r.y);
+          }
+        }
+      }
+    }
+    slot = 1;
+    // on to the next pair (warps 1 to 3 may run ahead: the merge buffers are written again only behind a barrier)
+    use.tile += n_here - 1;
+    use.next(P);
+  }
+}
+
+// The parts of one (sequence, query head) joined: a block of D threads, one value each.
+template <class T, int D>
+__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ PagedParams P) {
+  using S = Shape<D>;
+  __shared__ long long scratch[D + 1];
+  const int head = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  int per;
+  const long long total = scan_units<D>(P, scratch, per);
+  T* out = static_cast<T*>(P.a.out) + b * P.a.o_row_stride + head * P.a.o_head_stride;
+  const int ntile = (keys_of(P.a, b) + kUnit - 1) / kUnit;
+  if (ntile == 0) {
+    out[d] = static_cast<T>(0.f);
+    return;
+  }
+  const int pairs = P.a.pages.n_kv_heads * P.tiles;
+  long long at = scratch[b / per];
+  for (int i = b / per * per; i < b; ++i) at += (long long)((keys_of(P.a, i) + kUnit - 1) / kUnit) * pairs;
+  const int in_group = head % P.group, row = in_group % kRows;
+  const long long p0 = at + (long long)((head / P.group) * P.tiles + in_group / kRows) * ntile, p1 = p0 + ntile;
+  // block c's share is [total c / n, total (c + 1) / n): unit u is in share ((u + 1) n - 1) / total
+  const int c0 = (int)(((p0 + 1) * P.n_cta - 1) / total), c1 = (int)((p1 * P.n_cta - 1) / total);
+  if (c0 == c1) return;  // one block had it all and wrote it
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const long long u0 = total * c / P.n_cta, u1 = total * (c + 1) / P.n_cta;
+    if (u0 >= u1) continue;
+    const float* part = P.partial + ((long long)c * 2 + (u0 < p0 ? 1 : 0)) * S::kPartial;
+    const float pm = part[row], pl = part[kRows + row], po = part[2 * kRows + row * D + d];
+    const float top = fmaxf(m, pm), f = exp2f(m - top), g = exp2f(pm - top);
+    l = l * f + pl * g;
+    o = o * f + po * g;
+    m = top;
+  }
+  out[d] = static_cast<T>(o / l);
+}
+
+template <class T, int D>
+mk_status launch(const PagedParams& P, cudaStream_t s, std::string& err) {
+  using S = Shape<D>;
+  const bool full = P.group > 8;
+  auto kernel = full ? paged_kernel<T, D, true> : paged_kernel<T, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention attributes", err);
+  kernel<<<P.n_cta, kThreads, S::kSmem, s>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention launch", err);
+  join_kernel<T, D><<<dim3(P.a.n_q_heads, P.a.batch), D, 0, s>>>(P);
+  return cuda_result(cudaGetLastError(), "mk_paged_attention join launch", err);
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(int, int, int, int head_dim) {
+  return (size_t)kMaxCtas * 2 * (head_dim <= 64 ? Shape<64>::kPartial : Shape<128>::kPartial) * sizeof(float);
+}
+
+mk_status launch_paged(const mk_paged_attn_args& a, void* stream, std::string& err) {
+  PagedParams P;
+  P.a = a;
+  P.group = a.n_q_heads / a.pages.n_kv_heads;
+  P.tiles = (P.group + kRows - 1) / kRows;
+  const float scale = a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)a.pages.head_dim);
+  P.scale_log2 = scale * 1.4426950408889634f;
+  P.partial = static_cast<float*>(a.workspace);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention device query", err);
+  const int D = a.pages.head_dim;
+  P.n_cta = std::min(kMaxCtas, sms * (D == 64 ? Shape<64>::kBlocksPerSm : Shape<128>::kBlocksPerSm));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.pages.dtype == MK_DTYPE_BF16)
+    return D == 64 ? launch<__nv_bfloat16, 64>(P, s, err) : launch<__nv_bfloat16, 128>(P, s, err);
+  return D == 64 ? launch<__half, 64>(P, s, err) : launch<__half, 128>(P, s, err);
+}
+
+}  // namespace mk

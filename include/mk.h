@@ -418,6 +418,169 @@ double mk_plan_step_bytes(const mk_plan* p, int batch, const int* ctx_lens_host,
 
 void mk_plan_destroy(mk_plan* p);
 
+/* ------------------------------------------------------------------------
+ * Serving operators: what stands around a decode step.  They need no plan.
+ * mk_append_kv turns a projection's query and key rows to their positions and
+ * puts key and value rows into the cache, mk_prompt_attention attends whole
+ * prompts (or the next chunk of them) at once, mk_paged_attention attends one
+ * new token per sequence over a paged cache, and mk_process_logits applies
+ * penalties, biases and a grammar's mask to logits and chooses the tokens.
+ *
+ * For all four:
+ *  - every array is device memory of the current device; arrays named const
+ *    are not written;
+ *  - the call is one or two kernel launches on `stream`, asynchronous, with no
+ *    allocation, no synchronisation and no state kept from call to call; it
+ *    may be captured into a CUDA graph;
+ *  - sizes that only the device knows (lengths, page ids) are checked there: a
+ *    page id outside [0, n_pages), a length below zero or beyond what the
+ *    page table or the rows hold is never followed.  The rows concerned are
+ *    skipped (append) or see only the keys that are there (attention; a bad
+ *    page reads as zeros), and *status, where given, becomes
+ *    MK_ERR_DEVICE_BOUNDS.  The status word is written only then: the caller
+ *    clears it;
+ *  - MK_ERR_INVALID_ARG for null or misaligned pointers and sizes out of
+ *    range, MK_ERR_UNSUPPORTED for a valid request that is not implemented.
+ *    A call with nothing to do (no rows) returns MK_OK and launches nothing.
+ */
+#define MK_DTYPE_BF16 0
+#define MK_DTYPE_FP16 1
+#define MK_DTYPE_FP32 2   /* mk_logits_args.dtype only */
+
+/* A paged key/value cache.  Element (page, head, row, i) of either tensor is
+ * at page * page_stride + head * head_stride + row * row_stride + i; strides
+ * are in elements, multiples of 8, and both tensors start on 16 bytes.  Key t
+ * of sequence b is row t % page_size of page page_table[b][t / page_size].
+ * One layer of a decode plan's slot cache ([n_slots][n_kv_heads][max_ctx]
+ * [head_dim]) is a pool with one page of max_ctx rows per slot; its page table
+ * is the slot ids, one column. */
+typedef struct mk_kv_pages {
+  void* k;                /* post-RoPE keys */
+  void* v;
+  int dtype;              /* MK_DTYPE_BF16 or MK_DTYPE_FP16 */
+  int n_kv_heads, head_dim; /* head_dim 64 or 128 */
+  int n_pages, page_size; /* page_size >= 1 */
+  long long page_stride, head_stride, row_stride;
+  const int* page_table;  /* int32 [batch][table_stride]; entries past a sequence's last page are not read */
+  int table_width;        /* pages a row of the table can name */
+  int table_stride;       /* entries from one row to the next, >= table_width */
+} mk_kv_pages;
+
+/* Rotation and append.  Rows of q, k and v are the new tokens of all
+ * sequences, packed: sequence b's are rows cu_seqlens[b] .. cu_seqlens[b+1].
+ * Its i-th new token sits at position ctx_lens[b] + i; pair (p, p + D/2) of
+ * each query and key head turns by position * rope_theta^(-2p/D), computed in
+ * double (as the decode step does), products in fp32, one rounding at the end.  Key and value
+ * rows are stored at that position of the sequence's pages, the turned query
+ * rows in q_out.  Rows behind the last sequence are left as they are; two
+ * sequences must not name the same row of a page. */
+typedef struct mk_append_args {
+  mk_kv_pages pages;      /* written */
+  int batch, n_tokens;    /* sequences; rows of q, k and v */
+  int n_q_heads;          /* heads of q (0 with q NULL) */
+  const void* q;          /* [n_tokens][n_q_heads][head_dim], or NULL: no queries */
+  const void* k;          /* [n_tokens][n_kv_heads][head_dim] */
+  const void* v;          /* like k */
+  void* q_out;            /* like q; may be q itself (then with q's strides) */
+  long long q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride,
+      qo_row_stride, qo_head_stride; /* elements, multiples of 8 */
+  const int* cu_seqlens;  /* int32 [batch + 1], not decreasing, cu_seqlens[batch] <= n_tokens */
+  const int* ctx_lens;    /* int32 [batch]: tokens already cached */
+  double rope_theta;      /* rotary base; 0: no rotation */
+  int* status;            /* int32 or NULL */
+} mk_append_args;
+
+/* Attention over whole prompts.  Query rows are packed as in mk_append_args.
+ * The keys of sequence b are either packed too (pages.page_table NULL: rows
+ * cu_k[b] .. cu_k[b+1] of page 0, with n_pages 1, page_size = rows of k and
+ * v), or the first kv_lens[b] rows of its pages (page_size at least 128, or
+ * 16, 32 or 64).  With n queries and m keys, query i sees the keys
+ * j <= i + m - n (causal; the last query sees every key) or all m.  Query head
+ * h reads kv head h / (n_q_heads / n_kv_heads).  out = softmax(scale * q k^T) v
+ * with fp32 sums, probabilities rounded to the type for their product; a row that
+ * sees no key is zero.  A sequence's cached rows past kv_lens[b], and other
+ * sequences' rows, may hold anything; its own values must be finite, or rows
+ * before them may be NaN too.  Rows of out behind the last sequence are left as they are. */
+typedef struct mk_prompt_args {
+  mk_kv_pages pages;      /* read */
+  int batch, n_tokens;    /* sequences; rows of q and out */
+  int n_q_heads;          /* a multiple of n_kv_heads, at most 128 times it */
+  int causal;             /* 1 or 0 */
+  float scale;            /* 0 = 1 / sqrt(head_dim) */
+  const void* q;          /* [n_tokens][n_q_heads][head_dim] */
+  void* out;              /* like q */
+  long long q_row_stride, q_head_stride, o_row_stride, o_head_stride; /* elements, multiples of 8 */
+  const int* cu_q;        /* int32 [batch + 1]: query rows of each sequence */
+  const int* cu_k;        /* int32 [batch + 1]: key rows (packed keys) */
+  const int* kv_lens;     /* int32 [batch]: keys of each sequence (paged keys) */
+  int* status;            /* int32 or NULL */
+} mk_prompt_args;
+
+/* Attention of one new token per sequence over its first kv_lens[b] cached
+ * rows (the new token's own row among them).  The work is cut over the keys
+ * of all sequences in equal shares, whatever their lengths, and the parts of
+ * a (sequence, kv head) are joined through the workspace by a second kernel.
+ * kv_lens[b] = 0 gives a zero row.  Bit-identical from run to run. */
+typedef struct mk_paged_attn_args {
+  mk_kv_pages pages;      /* read */
+  int batch;              /* at most MK_PAGED_ATTN_MAX_BATCH */
+  int n_q_heads;          /* a multiple of n_kv_heads */
+  float scale;            /* 0 = 1 / sqrt(head_dim) */
+  const void* q;          /* [batch][n_q_heads][head_dim] */
+  void* out;              /* like q */
+  long long q_row_stride, q_head_stride, o_row_stride, o_head_stride; /* elements, multiples of 8 */
+  const int* kv_lens;     /* int32 [batch] */
+  void* workspace;        /* mk_paged_attention_workspace_bytes, 256-byte aligned; need not be cleared,
+                             not to be shared by calls that overlap on the device */
+  size_t workspace_bytes;
+  int* status;            /* int32 or NULL */
+} mk_paged_attn_args;
+#define MK_PAGED_ATTN_MAX_BATCH 4096
+
+/* Logits to tokens.  For row b and id v, with n(v) the times v stands in
+ * history[b][0 .. history_lens[b]) and s(v) those from prompt_lens[b] on (the
+ * answer so far), in this order and in fp32:
+ *   x = logits[b][v]
+ *   if n(v) > 0:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   x = x - frequency[b] * s(v) - presence[b] * (s(v) > 0)
+ *   x = x + sum of the row's bias values with this id
+ *   x = -infinity where the mask's bit v is 0, whatever x was
+ * out receives x; next_tokens[b] the id of the largest x (ties -> lowest id;
+ * NaN is not chosen), or -1 where no x is above -infinity.  Ids outside
+ * [0, vocab) in the history and the bias list are skipped.  Any of the arrays
+ * below may be NULL (no such step); out and next_tokens not both. */
+typedef struct mk_logits_args {
+  int rows, vocab;
+  int dtype;              /* of logits: MK_DTYPE_FP32, BF16 or FP16 */
+  const void* logits;     /* [rows][logits_stride] */
+  long long logits_stride;
+  float* out;             /* fp32 [rows][out_stride] or NULL; may be logits itself (fp32, same stride) */
+  long long out_stride;
+  int* next_tokens;       /* int32 [rows] or NULL */
+  const int* history;     /* int32 [rows][history_stride]: the prompt's ids, then the answer's */
+  int history_width;      /* ids a row of history holds */
+  long long history_stride;
+  const int* history_lens; /* int32 [rows]; NULL = history_width */
+  const int* prompt_lens; /* int32 [rows]; NULL = 0 */
+  const float* repetition; /* fp32 [rows], > 0 (1 = none) */
+  const float* frequency; /* fp32 [rows] */
+  const float* presence;  /* fp32 [rows] */
+  const int* bias_indptr; /* int32 [rows + 1]: row b's entries of bias_ids and bias_values */
+  const int* bias_ids;    /* int32 [bias_count] */
+  const float* bias_values; /* fp32 [bias_count]; equal ids of a row add up in list order */
+  int bias_count;
+  const unsigned* mask;   /* uint32 [rows][mask_stride]: bit v % 32 of word v / 32 set = id v allowed */
+  long long mask_stride;  /* words; 0 = one mask for all rows */
+  int* status;            /* int32 or NULL: bounds of history_lens and bias_indptr */
+} mk_logits_args;
+
+mk_status mk_append_kv(const mk_append_args* a, void* stream);
+mk_status mk_prompt_attention(const mk_prompt_args* a, void* stream);
+/* Workspace of mk_paged_attention (it does not grow with the lengths). */
+size_t mk_paged_attention_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim);
+mk_status mk_paged_attention(const mk_paged_attn_args* a, void* stream);
+mk_status mk_process_logits(const mk_logits_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
