@@ -1,94 +1,545 @@
 // prompt_attn.cu — mk_prompt_attention: attention of packed prompts over packed
-// or paged keys.
+// or paged keys, on tcgen05.
 //
-// A warp per (query row, head): its lanes hold the row's dimensions, the keys
-// pass one after the other with a running maximum and sum.  Right for every
-// case; bound by its instructions (a warp reduction per key).
+// Mathematics: out_i = sum_j p_ij v_j / sum_j p_ij, p_ij = 2^(c (q_i.k_j) - m_i),
+// c = scale log2 e, in one pass over the keys with a running reference m_i.
+// m_i follows the running maximum only when that has grown by more than 2^8:
+// the probabilities then stay below 2^8, exact in the same way, and the
+// accumulated output is rescaled a few times a row instead of at every tile.
+//
+// Rows: the G = n_q_heads / n_kv_heads query heads that share a kv head are
+// stacked, so a tile of 128 rows is floor(128 / G) tokens times G heads (one
+// TMA box [tokens][G][64]); a short prompt fills a tile G times better and the
+// causal diagonal is G times narrower than with one head per tile.
+//
+// A block holds two such tiles (256 rows) and streams the keys past both:
+//   warps 0-3 / 4-7: softmax of tile 0 / 1, a thread per row: S from TMEM to
+//                    registers, maximum, exponentials, P (16 bit) back to TMEM
+//                    over S, at the end O / l to global memory;
+//   warp 8:          one thread issues the MMAs, S = Q K^T (Q, K from shared
+//                    memory, both K-major) and O += P V (P from TMEM, V from
+//                    shared memory, its N = dimensions contiguous);
+//   warp 9:          TMA loads, K and V tiles of 128 keys in a ring.
+// While one tile is in its softmax, the other has the tensor pipe.
+//
+// Bound: at D = 128 the two products and the exponentials take the same time
+// (128 x 128 scores: 1,024 cycles of the tensor pipe, 1,024 of the MUFU); at
+// D = 64 the exponentials take twice the products' time.
+#include <cuda.h>
+
+#include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "serve.cuh"
 
 namespace mk {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kRows = 128;   // rows of a tile, keys of a tile
+constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
+constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait
+
+template <int D>
+struct Shape {
+  static constexpr int kTile = kRows * D * 2;        // bytes of 128 rows
+  static constexpr int kStages = D == 64 ? 8 : 4;    // ring of K and V tiles
+  static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024;
+};
 
 struct PromptParams {
+  CUtensorMap tq, tk, tv;
   mk_prompt_args a;
   float scale_log2;
+  int group, tokens;   // G; tokens of a row tile
+  int pairs;           // upper bound on row-tile pairs of all sequences
+  int span, per_span;  // keys of a page (or of all), key tiles that cover them
+  int box;             // key rows of a TMA box
+};
+
+struct Control {
+  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2];
+  uint32_t tmem;
+  int abort;
+  int warp_sum[kSoftmaxWarps];
+  int found;
+  int seq, pair;
+};
+
+// A whole warp waits for a phase; false (for all its lanes) after the limit or once another role has given up.
+__device__ __forceinline__ bool await_lane(Control& c, uint64_t* bar, uint32_t parity, int* status) {
+  if (mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&c.abort)) return false;
+    if (global_ns() - t0 > kWaitNs) {
+      *reinterpret_cast<volatile int*>(&c.abort) = 1;
+      if (status) *status = MK_ERR_DEVICE_TIMEOUT;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ bool await(Control& c, uint64_t* bar, uint32_t parity, int* status) {
+  return __all_sync(~0u, await_lane(c, bar, parity, status));
+}
+// Waits for copies in flight, whatever became of the other roles.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try(bar, parity) && global_ns() - t0 < kWaitNs) {}
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Shared-memory descriptor of an operand whose M or N is contiguous, under the
+// 128-byte swizzle: 64 elements (128 bytes) a row, a row per k; 8-k groups are
+// 1024 bytes apart (stride offset 64), blocks of 64 elements 16 KB (leading
+// offset 1024).  A 16-k step is the descriptor plus 128 (2048 bytes).
+__device__ __forceinline__ uint64_t desc_mn_sw128(const void* tile) {
+  const uint64_t a = (smem_u32(tile) >> 4) & 0x3FFFull;
+  return a | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16 instruction descriptor: fp32 D, A and B bf16 (format 1) or fp16
+// (format 0), bit 16: B with N contiguous.
+template <class T>
+__device__ constexpr uint32_t idesc(int n, bool b_mn) {
+  const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] . B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+
+#define MK_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define MK_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// 32 consecutive columns of the thread's TMEM lane (no wait)
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : MK_R8(r, 0), MK_R8(r, 8), MK_R8(r, 16), MK_R8(r, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      MK_W8(r, 0), MK_W8(r, 8), MK_W8(r, 16), MK_W8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      MK_W8(r, 0), MK_W8(r, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One sequence: its query rows, key rows and where they lie.
+struct Seq {
+  int q0, n;   // first query row, queries
+  int k0, m;   // first key row (packed), keys
+  __device__ __forceinline__ void load(const PromptParams& P, int b) {
+    const mk_prompt_args& a = P.a;
+    const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1);
+    q0 = min(max(c0, 0), a.n_tokens);
+    n = max(min(c1, a.n_tokens), q0) - q0;
+    bool fine = c0 == q0 && c1 == q0 + n;
+    if (a.pages.page_table) {
+      const int cap = a.pages.table_width * a.pages.page_size, l = __ldg(a.kv_lens + b);
+      k0 = 0;
+      m = min(max(l, 0), cap);
+      fine = fine && l == m;
+    } else {
+      const int e0 = __ldg(a.cu_k + b), e1 = __ldg(a.cu_k + b + 1);
+      k0 = min(max(e0, 0), a.pages.page_size);
+      m = max(min(e1, a.pages.page_size), k0) - k0;
+      fine = fine && e0 == k0 && e1 == k0 + m;
+    }
+    if (!fine) report_bounds(a.status);
+  }
+  // keys that query i sees
+  __device__ __forceinline__ int limit(const PromptParams& P, int i) const {
+    return P.a.causal ? min(m, max(0, i + 1 + m - n)) : m;
+  }
 };
 
 template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32) prompt_kernel(const __grid_constant__ PromptParams P) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams P) {
+  using S = Shape<D>;
+  constexpr int HALVES = D / 64;
+  extern __shared__ unsigned char raw[];
+  __shared__ Control c;
+  unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  unsigned char* sq = smem;                  // [2 tiles][HALVES][128][64]
+  unsigned char* ring = smem + 2 * S::kTile; // [kStages][HALVES][128][64]
   const mk_prompt_args& a = P.a;
-  const mk_kv_pages& g = a.pages;
-  const int lane = threadIdx.x & 31, head = blockIdx.y;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= a.n_tokens) return;
-  int b = 0;
-  for (int i = lane; i < a.batch; i += 32) b += __ldg(a.cu_q + i + 1) <= t;
-  b = __reduce_add_sync(~0u, b);
-  if (b >= a.batch) return;
-  int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
-  if (q0 > t) return;
-  if (q0 < 0 || q1 > a.n_tokens) {
-    report_bounds(a.status);
-    q0 = max(q0, 0);
-    q1 = min(q1, a.n_tokens);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kvh = blockIdx.x % a.pages.n_kv_heads;
+  const int want = P.pairs - 1 - (int)(blockIdx.x / a.pages.n_kv_heads);  // long rows (the last) first
+
+  // ---- which sequence and pair of row tiles: counted over the sequences, 256 at a time
+  if (tid == 0) {
+    c.abort = 0;
+    c.found = 0;
   }
-  int k0 = 0, m;
-  if (g.page_table) {
-    const int cap = g.table_width * g.page_size;
-    m = __ldg(a.kv_lens + b);
-    if (m < 0 || m > cap) {
-      report_bounds(a.status);
-      m = m < 0 ? 0 : cap;
+  __syncthreads();
+  int base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kSoftmaxWarps * 32) {
+    int mine = 0, sum = 0;
+    if (warp < kSoftmaxWarps) {
+      const int b = b0 + tid;
+      if (b < a.batch) {
+        const int q0 = min(max(__ldg(a.cu_q + b), 0), a.n_tokens), q1 = min(__ldg(a.cu_q + b + 1), a.n_tokens);
+        mine = (max(q1 - q0, 0) + 2 * P.tokens - 1) / (2 * P.tokens);
+      }
+      sum = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(~0u, sum, d);
+        if (lane >= d) sum += o;
+      }
+      if (lane == 31) c.warp_sum[warp] = sum;
+    }
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kSoftmaxWarps; ++w) {
+      if (w < warp) sum += c.warp_sum[w];
+      total += c.warp_sum[w];
+    }
+    if (warp < kSoftmaxWarps && want >= base + sum - mine && want < base + sum) {
+      c.seq = b0 + tid;
+      c.pair = want - (base + sum - mine);
+      c.found = 1;
+    }
+    __syncthreads();
+    base += total;
+    if (c.found) break;
+  }
+  if (!c.found) return;
+
+  Seq s;
+  s.load(P, c.seq);
+  const int first = c.pair * 2 * P.tokens;  // the block's first query
+  int tiles[2];                             // key tiles of each row tile
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(s.n, first + (t + 1) * P.tokens) - 1;
+    const int seen = last >= first + t * P.tokens ? s.limit(P, last) : 0;
+    const int full = seen > 0 ? (seen - 1) / P.span : 0;
+    tiles[t] = seen > 0 ? full * P.per_span + (seen - full * P.span + kRows - 1) / kRows : 0;
+  }
+  const int n_tiles = max(tiles[0], tiles[1]);
+
+  if (tid == 0) {
+    mbar_init(&c.q_full, 1);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&c.kv_full[i], 1);
+      mbar_init(&c.kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&c.s_full[t], 1);
+      mbar_init(&c.p_full[t], 4);
+      mbar_init(&c.pv_done[t], 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kSoftmaxWarps) tmem_alloc(&c.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem;  // S0, S1 at columns 0 and 128, O0, O1 at 256 and 256 + D
+
+  if (warp == kSoftmaxWarps + 1) {
+    // ---- loads
+    if (n_tiles > 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&c.q_full, 2u * HALVES * P.tokens * P.group * 128);
+        for (int t = 0; t < 2; ++t)
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_3d(sq + t * S::kTile + h * (kRows * 128), &P.tq, 64 * h, kvh * P.group, s.q0 + first + t * P.tokens,
+                        &c.q_full);
+      }
+      const int boxes = kRows / P.box;
+      const int pages = a.pages.page_table ? (s.m + a.pages.page_size - 1) / a.pages.page_size : 1;
+      int issued = 0;
+      bool fine = true;
+      for (int i = 0; i < 2 * n_tiles && fine; ++i) {
+        const int stage = i % S::kStages, j = i >> 1;
+        if (i >= S::kStages) fine = await(c, &c.kv_empty[stage], (i / S::kStages - 1) & 1, a.status);
+        if (!fine) break;
+        if (lane == 0) mbar_arrive_expect_tx(&c.kv_full[stage], S::kTile);
+        __syncwarp();
+        if (lane < boxes) {
+          int page = 0, row;
+          if (!a.pages.page_table) {
+            row = s.k0 + j * kRows;
+          } else {
+            const int key = (j / P.per_span) * P.span + (j % P.per_span) * kRows + lane * P.box;
+            const int at = key / a.pages.page_size;
+            row = key % a.pages.page_size;
+            page = at < pages ? page_of(a.pages, c.seq, at, a.status) : -1;
+            if (page < 0) page = a.pages.n_pages;  // out of range: the box reads as zeros
+          }
+          unsigned char* dst = ring + stage * S::kTile + lane * P.box * 128;
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_4d(dst + h * (kRows * 128), (i & 1) ? &P.tv : &P.tk, 64 * h, row, kvh, page, &c.kv_full[stage]);
+        }
+        __syncwarp();
+        issued = i + 1;
+      }
+      // no copy is in flight when the block leaves, even if another role has given up
+      drain(&c.q_full, 0);
+      for (int i = max(0, issued - S::kStages); i < issued; ++i) drain(&c.kv_full[i % S::kStages], (i / S::kStages) & 1);
+    }
+  } else if (warp == kSoftmaxWarps) {
+    // ---- MMAs: the warp waits together, lane 0 issues
+    if (n_tiles > 0) {
+      constexpr uint32_t id_qk = idesc<T>(kRows, false), id_pv = idesc<T>(D, true);
+      bool fine = await(c, &c.q_full, 0, a.status);
+      auto qk = [&](int t, int j) {
+        const int stage = (2 * j) % S::kStages;
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int off = (k / 4) * (kRows * 128);
+            umma_bf16(tmem + 128u * t, umma_desc_sw128(sq + t * S::kTile + off) + 2u * (k % 4),
+                      umma_desc_sw128(ring + stage * S::kTile + off) + 2u * (k % 4), id_qk, k ? 1u : 0u);
+          }
+          umma_commit(&c.s_full[t]);
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int t, int j) {
+        const int stage = (2 * j + 1) % S::kStages;
+        if (lane == 0) {
+          const uint64_t v = desc_mn_sw128(ring + stage * S::kTile);
+#pragma unroll
+          for (int k = 0; k < kRows / 16; ++k)
+            umma_ts(tmem + 256u + D * t, tmem + 128u * t + 8u * k, v + 128u * k, id_pv, (j | k) ? 1u : 0u);
+          umma_commit(&c.pv_done[t]);
+        }
+        __syncwarp();
+      };
+      fine = fine && await(c, &c.kv_full[0], 0, a.status);
+      tc_fence_after();
+      if (fine) {
+        for (int t = 0; t < 2; ++t)
+          if (tiles[t] > 0) qk(t, 0);
+        if (lane == 0) umma_commit(&c.kv_empty[0]);
+      }
+      for (int j = 0; j < n_tiles && fine; ++j) {
+        const int iv = 2 * j + 1, ik = 2 * j + 2;
+        fine = await(c, &c.kv_full[iv % S::kStages], (iv / S::kStages) & 1, a.status);
+        if (!fine) break;
+        {
+          // rows behind the sequence's last key may hold anything, NaN too, and meet probabilities of zero: cleared
+          const int sub = (j % P.per_span) * kRows;
+          const int live = s.m - ((j / P.per_span) * P.span + sub);
+          if (live < kRows) {
+            for (int i = lane; i < (kRows - max(live, 0)) * 8 * HALVES; i += 32) {
+              const int h = i / ((kRows - max(live, 0)) * 8), r = i % ((kRows - max(live, 0)) * 8);
+              *reinterpret_cast<uint4*>(ring + (iv % S::kStages) * S::kTile + h * (kRows * 128) + max(live, 0) * 128 + r * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        bool k_here = false;
+        for (int t = 0; t < 2 && fine; ++t) {
+          if (j < tiles[t]) {
+            fine = await(c, &c.p_full[t], j & 1, a.status);
+            if (!fine) break;
+            tc_fence_after();
+            pv(t, j);
+          }
+          if (j + 1 < tiles[t]) {
+            if (!k_here) fine = await(c, &c.kv_full[ik % S::kStages], (ik / S::kStages) & 1, a.status);
+            if (!fine) break;
+            tc_fence_after();
+            k_here = true;
+            qk(t, j + 1);
+          }
+        }
+        if (lane == 0) {
+          umma_commit(&c.kv_empty[iv % S::kStages]);
+          if (j + 1 < n_tiles) umma_commit(&c.kv_empty[ik % S::kStages]);
+        }
+        __syncwarp();
+      }
     }
   } else {
-    k0 = __ldg(a.cu_k + b);
-    int k1 = __ldg(a.cu_k + b + 1);
-    if (k0 < 0 || k1 > g.page_size || k1 < k0) {
-      report_bounds(a.status);
-      k0 = min(max(k0, 0), g.page_size);
-      k1 = max(min(k1, g.page_size), k0);
+    // ---- softmax: a thread per row
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + 128u * t;
+    const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + 256u + D * t;
+    const int token = first + t * P.tokens + r / P.group;
+    const bool row_live = r < P.tokens * P.group && token < s.n;
+    const int limit = row_live ? s.limit(P, token) : 0;
+    float m = 0.f, l = 0.f;
+    bool fine = true;
+    for (int j = 0; j < tiles[t] && fine; ++j) {
+      fine = await(c, &c.s_full[t], j & 1, a.status);
+      if (!fine) break;
+      tc_fence_after();
+      uint32_t x[kRows];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+      tmem_wait_ld();
+      const int sub = (j % P.per_span) * kRows;
+      const int live = min(limit - ((j / P.per_span) * P.span + sub), P.span - sub);  // columns the row sees
+      if (__any_sync(~0u, live < kRows)) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (i >= live) x[i] = 0xff800000u;
+      }
+      float top = __uint_as_float(x[0]);
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) top = fmaxf(top, __uint_as_float(x[i]));
+      top *= P.scale_log2;
+      if (j == 0) {
+        m = top == -INFINITY ? 0.f : top;
+      } else if (__any_sync(~0u, top > m + kSlack)) {
+        fine = await(c, &c.pv_done[t], (j - 1) & 1, a.status);
+        if (!fine) break;
+        tc_fence_after();
+        const float up = top > m + kSlack ? top : m, f = ex2(m - up);
+        m = up;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + i, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st32(to + i, o);
+        }
+      }
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kRows; i += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float u = ex2(fmaf(__uint_as_float(x[i + 2 * e]), P.scale_log2, -m));
+          const float v = ex2(fmaf(__uint_as_float(x[i + 2 * e + 1]), P.scale_log2, -m));
+          sum[0] += u;
+          sum[1] += v;
+          p[e] = Elem<T>::pack(u, v);
+        }
+        tmem_st16(ts + i / 2, p);
+      }
+      l += sum[0] + sum[1];
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.p_full[t]);
     }
-    m = k1 - k0;
+    if (tiles[t] > 0 && fine) {
+      fine = await(c, &c.pv_done[t], (tiles[t] - 1) & 1, a.status);
+      tc_fence_after();
+    }
+    if (fine) {
+      const float inv = limit > 0 ? 1.f / l : 0.f;
+      T* out = static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.o_row_stride +
+               (long long)(kvh * P.group + r % P.group) * a.o_head_stride;
+#pragma unroll
+      for (int i = 0; i < D; i += 32) {
+        uint32_t o[32];
+        if (tiles[t] > 0) {
+          tmem_ld32(to + i, o);
+          tmem_wait_ld();
+        }
+        if (row_live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (limit > 0) {
+              w.x = Elem<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+              w.y = Elem<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+              w.z = Elem<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+              w.w = Elem<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+            }
+            *reinterpret_cast<uint4*>(out + i + e) = w;
+          }
+        }
+      }
+    }
   }
-  const int seen = a.causal ? min(m, max(0, t - q0 + 1 + m - (q1 - q0))) : m;
-  const int kvh = head / (a.n_q_heads / g.n_kv_heads);
-  float q[E], o[E] = {};
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    q[e] = static_cast<float>(static_cast<const T*>(a.q)[t * a.q_row_stride + head * a.q_head_stride + lane * E + e]) * P.scale_log2;
-  float top = -INFINITY, sum = 0.f;
-  for (int j = 0; j < seen; ++j) {
-    long long off = (long long)(k0 + j) * g.row_stride;
-    bool live = true;
-    if (g.page_table) {
-      const int page = page_of(g, b, j / g.page_size, a.status);
-      live = page >= 0;
-      off = live ? page * g.page_stride + (long long)(j % g.page_size) * g.row_stride : 0;
-    }
-    off += kvh * g.head_stride + lane * E;
-    float s = 0.f, v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      s += live ? q[e] * static_cast<float>(static_cast<const T*>(g.k)[off + e]) : 0.f;
-      v[e] = live ? static_cast<float>(static_cast<const T*>(g.v)[off + e]) : 0.f;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    const float up = fmaxf(top, s), f = exp2f(top - up), p = exp2f(s - up);
-    sum = sum * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * v[e];
-    top = up;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftmaxWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  const float inv = seen > 0 ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    static_cast<T*>(a.out)[t * a.o_row_stride + head * a.o_head_stride + lane * E + e] = static_cast<T>(o[e] * inv);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+// A map of 16-bit elements [dims...] with element strides (of dimension 1 on), read in boxes of 64 x box under the
+// 128-byte swizzle.  A dimension of one element has no stride of its own.
+bool encode(CUtensorMap* map, int dtype, const void* p, int rank, const long long* dims, const long long* strides,
+            const int* box) {
+  EncodeTiledFn enc = encode_tiled();
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    if (i) st[i - 1] = (cuuint64_t)(dims[i] == 1 ? dims[0] : strides[i - 1]) * 2;
+  }
+  return enc && enc(map, dtype == MK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                    const_cast<void*>(p), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int D>
+mk_status launch(const PromptParams& P, cudaStream_t s, std::string& err) {
+  auto kernel = prompt_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+  if (e != cudaSuccess) return cuda_result(e, "mk_prompt_attention attributes", err);
+  kernel<<<P.pairs * P.a.pages.n_kv_heads, kThreads, Shape<D>::kSmem, s>>>(P);
+  return cuda_result(cudaGetLastError(), "mk_prompt_attention launch", err);
 }
 
 }  // namespace
@@ -96,18 +547,44 @@ __global__ void __launch_bounds__(kWarps * 32) prompt_kernel(const __grid_consta
 mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err) {
   PromptParams P;
   P.a = a;
-  const int D = a.pages.head_dim;
+  const mk_kv_pages& g = a.pages;
+  const int D = g.head_dim;
   P.scale_log2 = (a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid((a.n_tokens + kWarps - 1) / kWarps, a.n_q_heads);
-  if (a.pages.dtype == MK_DTYPE_BF16) {
-    if (D == 64) prompt_kernel<__nv_bfloat16, 64><<<grid, kWarps * 32, 0, s>>>(P);
-    else prompt_kernel<__nv_bfloat16, 128><<<grid, kWarps * 32, 0, s>>>(P);
-  } else {
-    if (D == 64) prompt_kernel<__half, 64><<<grid, kWarps * 32, 0, s>>>(P);
-    else prompt_kernel<__half, 128><<<grid, kWarps * 32, 0, s>>>(P);
+  P.group = a.n_q_heads / g.n_kv_heads;
+  P.tokens = kRows / P.group;
+  const long long pairs = (long long)a.n_tokens / (2 * P.tokens) + a.batch;
+  if (pairs * g.n_kv_heads > 0x7fffffffll) {
+    err = "too many row tiles for one launch";
+    return MK_ERR_UNSUPPORTED;
   }
-  return cuda_result(cudaGetLastError(), "mk_prompt_attention launch", err);
+  P.pairs = (int)pairs;
+  const bool paged = g.page_table != nullptr;
+  P.box = paged && g.page_size < kRows ? g.page_size : kRows;
+  P.span = paged ? std::max(g.page_size, kRows) : std::max(g.page_size, 1);
+  P.per_span = (P.span + kRows - 1) / kRows;
+  {
+    const long long dims[3] = {D, a.n_q_heads, a.n_tokens}, strides[2] = {a.q_head_stride, a.q_row_stride};
+    const int box[3] = {64, P.group, P.tokens};
+    if (!encode(&P.tq, g.dtype, a.q, 3, dims, strides, box)) {
+      err = "the driver takes no tensor map of q's strides";
+      return MK_ERR_UNSUPPORTED;
+    }
+  }
+  // (no keys at all: nothing is loaded, the maps are those of q)
+  P.tk = P.tv = P.tq;
+  if (g.n_pages > 0 && g.page_size > 0) {
+    const long long dims[4] = {D, g.page_size, g.n_kv_heads, g.n_pages};
+    const long long strides[3] = {g.row_stride, g.head_stride, g.page_stride};
+    const int box[4] = {64, P.box, 1, 1};
+    if (!encode(&P.tk, g.dtype, g.k, 4, dims, strides, box) || !encode(&P.tv, g.dtype, g.v, 4, dims, strides, box)) {
+      err = "the driver takes no tensor map of the keys' strides";
+      return MK_ERR_UNSUPPORTED;
+    }
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (g.dtype == MK_DTYPE_BF16)
+    return D == 64 ? launch<__nv_bfloat16, 64>(P, s, err) : launch<__nv_bfloat16, 128>(P, s, err);
+  return D == 64 ? launch<__half, 64>(P, s, err) : launch<__half, 128>(P, s, err);
 }
 
 }  // namespace mk
