@@ -369,79 +369,99 @@ class MoELayer:
 
 
 # ---------------------------------------------------------------- serving operators on tensors
+# (Single-token calls take a few microseconds on the device, so the checks here read each property of a tensor once
+# and leave what the C ABI checks to it.)
 def _refuse(what):
     raise MkError(MK_ERR_INVALID_ARG, what)
 
 
+_DTYPES = {}
+
+
 def _dtypes():
-    import torch
-    return {torch.bfloat16: MK_DTYPE_BF16, torch.float16: MK_DTYPE_FP16, torch.float32: MK_DTYPE_FP32}
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: MK_DTYPE_BF16, torch.float16: MK_DTYPE_FP16, torch.float32: MK_DTYPE_FP32})
+    return _DTYPES
 
 
-def _on(device, **tensors):
+def _on(device, *tensors):
     """Every given tensor is on ``device`` (a CUDA device)."""
     if device.type != "cuda":
         _refuse("the tensors must be on a CUDA device")
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.device != device:
-            _refuse(f"{name} is on {t.device}, not on {device}")
+            _refuse(f"a tensor {list(t.shape)} is on {t.device}, the others on {device}")
 
 
 def _rows(name, t, shape, dtype):
-    """Strides (row, head) of a [rows][heads][head_dim] tensor whose last dimension is dense."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    """Address and strides (row, head) of a [rows][heads][head_dim] tensor whose last dimension is dense."""
+    if t.dtype != dtype or t.shape != shape:
         _refuse(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    row, head, one = t.stride()
+    if one != 1 and shape[2] > 1:
         _refuse(f"{name}: the last dimension must be dense")
     # (the stride of a dimension of size 1 is not used)
-    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
-def _array(name, t, dtype, *shape):
-    """A dense array of exactly this shape (None: not given)."""
+def _array(name, t, dtype, n):
+    """Address of a dense array of n values (0: not given)."""
     if t is None:
         return 0
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        _refuse(f"{name} must be a dense {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    return _ptr(t)
+    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+        _refuse(f"{name} must be a dense {dtype} [{n}], not {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
 
 
-def _pages(k, v, page_table, batch):
-    """mk_kv_pages of k, v [n_pages][n_kv_heads][page_size][head_dim] and page_table int32 [batch][width]."""
+def _pages(p, k, v, page_table, batch):
+    """Fill mk_kv_pages from k, v [n_pages][n_kv_heads][page_size][head_dim] and page_table int32 [batch][width]."""
     import torch
-    if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+    shape, strides, dtype = k.shape, k.stride(), k.dtype
+    if len(shape) != 4 or v.shape != shape or v.dtype != dtype or dtype not in (torch.bfloat16, torch.float16):
         _refuse("k and v pages must both be bf16 or fp16 [n_pages][n_kv_heads][page_size][head_dim]")
-    used = [i for i in range(3) if k.shape[i] > 1]
-    if (k.shape[3] > 1 and (k.stride(3) != 1 or v.stride(3) != 1)) or any(k.stride(i) != v.stride(i) for i in used):
-        _refuse("k and v pages must have the same strides and a dense last dimension")
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch or
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        _refuse("page_table must be int32 [batch][width] with dense rows")
-    p = mk_kv_pages()
-    p.k, p.v, p.dtype = _ptr(k), _ptr(v), _dtypes()[k.dtype]
-    p.n_pages, p.n_kv_heads, p.page_size, p.head_dim = k.shape
-    p.page_stride, p.head_stride, p.row_stride = (k.stride(i) if i in used else 0 for i in range(3))
-    p.page_table, p.table_width = _ptr(page_table), page_table.shape[1]
-    p.table_stride = page_table.stride(0) if batch > 1 else page_table.shape[1]
-    return p
+    if 1 in shape or v.stride() != strides:  # (the stride of a dimension of size 1 is not used)
+        strides, other = ([0 if n == 1 else st for n, st in zip(shape, t.stride())] for t in (k, v))
+        if strides != other:
+            _refuse("k and v pages must have the same strides")
+    if strides[3] != 1:
+        _refuse("k and v pages must have a dense last dimension")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch:
+        _refuse("page_table must be int32 [batch][width]")
+    width = page_table.shape[1]
+    stride, one = page_table.stride()
+    if one != 1 and width > 1:
+        _refuse("page_table must have dense rows")
+    p.k, p.v, p.dtype = k.data_ptr(), v.data_ptr(), _dtypes()[dtype]
+    p.n_pages, p.n_kv_heads, p.page_size, p.head_dim = shape
+    p.page_stride, p.head_stride, p.row_stride = strides[0], strides[1], strides[2]
+    p.page_table, p.table_width, p.table_stride = page_table.data_ptr(), width, stride if batch > 1 else width
 
 
 class _launch_on:
-    """The stream a call goes to (``stream``, or the device's current one) with its device current."""
+    """The stream a call goes to (``stream``, or the device's current one), made current with its device."""
 
     def __init__(self, device, stream):
         import torch
         if stream is not None and stream.device != device:
             _refuse(f"the stream is on {stream.device}, the tensors on {device}")
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        self._scope = torch.cuda.stream(self.stream)  # makes the stream's device current too
+        self.scope = None
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+            if torch.cuda.current_device() != device.index:
+                self.scope = torch.cuda.device(device)
+        else:
+            self.scope = torch.cuda.stream(stream)  # (outputs made here belong to it)
+        self.raw = stream.cuda_stream
 
     def __enter__(self):
-        self._scope.__enter__()
-        return self.stream.cuda_stream
+        if self.scope is not None:
+            self.scope.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
-        return self._scope.__exit__(*exc)
+        if self.scope is not None:
+            self.scope.__exit__(*exc)
 
 
 def append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_theta=10000.0, q_out=None, status=None,
@@ -456,31 +476,33 @@ def append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_
     allowed), or a new tensor, whose rows behind the last sequence are not written.  ``status``: int32 [1],
     see include/mk.h."""
     import torch
+    device = k.device
+    _on(device, q, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, q_out, status)
     if k.dim() != 3:
         _refuse("k must be [tokens][n_kv_heads][head_dim]")
-    batch = ctx_lens.numel()
-    _on(k.device, q=q, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, ctx_lens=ctx_lens,
-        cu_seqlens=cu_seqlens, q_out=q_out, status=status)
+    batch, shape, dtype = ctx_lens.numel(), k.shape, k.dtype
     a = mk_append_args()
-    a.pages = _pages(k_pages, v_pages, page_table, batch)
-    T, hkv, D = k.shape
-    a.batch, a.n_tokens = batch, T
-    a.k_row_stride, a.k_head_stride = _rows("k", k, (T, k_pages.shape[1], k_pages.shape[3]), k_pages.dtype)
-    a.v_row_stride, a.v_head_stride = _rows("v", v, k.shape, k.dtype)
-    a.k, a.v = _ptr(k), _ptr(v)
+    p = a.pages
+    _pages(p, k_pages, v_pages, page_table, batch)
+    if k_pages.dtype != dtype or p.n_kv_heads != shape[1] or p.head_dim != shape[2]:
+        _refuse(f"k {dtype} {list(shape)} does not match the pages {k_pages.dtype} {list(k_pages.shape)}")
+    a.batch, a.n_tokens = batch, shape[0]
+    a.k, a.k_row_stride, a.k_head_stride = _rows("k", k, shape, dtype)
+    a.v, a.v_row_stride, a.v_head_stride = _rows("v", v, shape, dtype)
     a.ctx_lens = _array("ctx_lens", ctx_lens, torch.int32, batch)
     a.cu_seqlens = _array("cu_seqlens", cu_seqlens, torch.int32, batch + 1)
     a.status = _array("status", status, torch.int32, 1)
-    a.rope_theta = float(rope_theta or 0.0)
-    with _launch_on(k.device, stream) as s:
+    a.rope_theta = rope_theta or 0.0
+    with _launch_on(device, stream) as s:
         if q is not None:
             if q.dim() != 3:
                 _refuse("q must be [tokens][n_q_heads][head_dim]")
-            a.q_row_stride, a.q_head_stride = _rows("q", q, (T, q.shape[1], D), k.dtype)
+            qshape = torch.Size((shape[0], q.shape[1], shape[2]))
+            a.q, a.q_row_stride, a.q_head_stride = _rows("q", q, qshape, dtype)
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            a.qo_row_stride, a.qo_head_stride = _rows("q_out", q_out, q.shape, q.dtype)
-            a.n_q_heads, a.q, a.q_out = q.shape[1], _ptr(q), _ptr(q_out)
+                q_out = q.new_empty(qshape)
+            a.q_out, a.qo_row_stride, a.qo_head_stride = _rows("q_out", q_out, qshape, dtype)
+            a.n_q_heads = qshape[1]
         elif q_out is not None:
             _refuse("q_out without q")
         mk_append_kv(a, s)
@@ -497,41 +519,43 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, page_table=None, kv_lens=None, ca
     sequence sees all its keys, each one before it one less.  ``scale`` defaults to 1 / sqrt(D).  Returns ``out``, or
     a new tensor, whose rows behind the last sequence are not written."""
     import torch
-    if q.dim() != 3:
+    device = q.device
+    _on(device, k, v, cu_q, cu_k, page_table, kv_lens, out, status)
+    shape, dtype, batch = q.shape, q.dtype, cu_q.numel() - 1
+    if len(shape) != 3:
         _refuse("q must be [tokens][n_q_heads][head_dim]")
-    batch = cu_q.numel() - 1
-    _on(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k, page_table=page_table, kv_lens=kv_lens, out=out, status=status)
     a = mk_prompt_args()
+    p = a.pages
     if page_table is not None:
         if kv_lens is None or cu_k is not None:
             _refuse("paged keys take kv_lens, not cu_k")
         if page_table.numel() == 0 and batch > 0:
             _refuse("page_table names no pages")
-        a.pages = _pages(k, v, page_table, batch)
+        _pages(p, k, v, page_table, batch)
         a.kv_lens = _array("kv_lens", kv_lens, torch.int32, batch)
     else:
         if kv_lens is not None:
             _refuse("packed keys take cu_k, not kv_lens")
-        if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+        kshape = k.shape
+        if len(kshape) != 3 or k.dtype not in (torch.bfloat16, torch.float16):
             _refuse("k and v must both be bf16 or fp16 [tokens][n_kv_heads][head_dim]")
-        p = a.pages
-        p.row_stride, p.head_stride = _rows("k", k, k.shape, k.dtype)
-        if _rows("v", v, k.shape, k.dtype) != (p.row_stride, p.head_stride):
+        p.k, p.row_stride, p.head_stride = _rows("k", k, kshape, k.dtype)
+        p.v, row, head = _rows("v", v, kshape, k.dtype)
+        if row != p.row_stride or head != p.head_stride:
             _refuse("k and v must have the same strides")
-        p.k, p.v, p.dtype, p.n_pages = _ptr(k), _ptr(v), _dtypes()[k.dtype], 1
-        p.page_size, p.n_kv_heads, p.head_dim = k.shape
+        p.dtype, p.n_pages = _dtypes()[k.dtype], 1
+        p.page_size, p.n_kv_heads, p.head_dim = kshape
         a.cu_k = _array("cu_k", cu_q if cu_k is None else cu_k, torch.int32, batch + 1)
-    T, hq, D = q.shape
-    a.batch, a.n_tokens, a.n_q_heads, a.causal, a.scale = batch, T, hq, int(bool(causal)), _scale(scale)
-    a.q_row_stride, a.q_head_stride = _rows("q", q, (T, hq, a.pages.head_dim), k.dtype)
-    a.q = _ptr(q)
+    if k.dtype != dtype or p.head_dim != shape[2]:
+        _refuse(f"q {dtype} {list(shape)} does not match k {k.dtype} {list(k.shape)}")
+    a.batch, a.n_tokens, a.n_q_heads, a.causal, a.scale = batch, shape[0], shape[1], bool(causal), _scale(scale)
+    a.q, a.q_row_stride, a.q_head_stride = _rows("q", q, shape, dtype)
     a.cu_q = _array("cu_q", cu_q, torch.int32, batch + 1)
     a.status = _array("status", status, torch.int32, 1)
-    with _launch_on(q.device, stream) as s:
+    with _launch_on(device, stream) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        a.o_row_stride, a.o_head_stride = _rows("out", out, q.shape, q.dtype)
-        a.out = _ptr(out)
+            out = q.new_empty(shape)
+        a.out, a.o_row_stride, a.o_head_stride = _rows("out", out, shape, dtype)
         mk_prompt_attention(a, s)
     return out
 
@@ -545,29 +569,30 @@ def paged_attention(q, k_pages, v_pages, page_table, kv_lens, scale=None, out=No
     256-byte aligned (a torch allocation is), not to be shared by calls that overlap; by default one is allocated.
     Returns ``out`` [B][Hq][D], or a new tensor."""
     import torch
-    if q.dim() != 3:
+    device = q.device
+    _on(device, k_pages, v_pages, page_table, kv_lens, out, workspace, status)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
         _refuse("q must be [batch][n_q_heads][head_dim]")
-    B, hq, D = q.shape
-    _on(q.device, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens, out=out,
-        workspace=workspace, status=status)
     a = mk_paged_attn_args()
-    a.pages = _pages(k_pages, v_pages, page_table, B)
-    a.batch, a.n_q_heads, a.scale = B, hq, _scale(scale)
-    a.q_row_stride, a.q_head_stride = _rows("q", q, (B, hq, k_pages.shape[3]), k_pages.dtype)
-    a.q = _ptr(q)
-    a.kv_lens = _array("kv_lens", kv_lens, torch.int32, B)
+    p = a.pages
+    _pages(p, k_pages, v_pages, page_table, shape[0])
+    if k_pages.dtype != dtype or p.head_dim != shape[2]:
+        _refuse(f"q {dtype} {list(shape)} does not match the pages {k_pages.dtype} {list(k_pages.shape)}")
+    a.batch, a.n_q_heads, a.scale = shape[0], shape[1], _scale(scale)
+    a.q, a.q_row_stride, a.q_head_stride = _rows("q", q, shape, dtype)
+    a.kv_lens = _array("kv_lens", kv_lens, torch.int32, shape[0])
     a.status = _array("status", status, torch.int32, 1)
-    with _launch_on(q.device, stream) as s:
+    with _launch_on(device, stream) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = q.new_empty(shape)
+        a.out, a.o_row_stride, a.o_head_stride = _rows("out", out, shape, dtype)
         if workspace is None:
-            workspace = torch.empty(mk_paged_attention_workspace_bytes(B, hq, k_pages.shape[1], D), dtype=torch.uint8,
-                                    device=q.device)
-        a.o_row_stride, a.o_head_stride = _rows("out", out, q.shape, q.dtype)
-        a.out = _ptr(out)
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            workspace = torch.empty(mk_paged_attention_workspace_bytes(shape[0], shape[1], p.n_kv_heads, shape[2]),
+                                    dtype=torch.uint8, device=device)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             _refuse("workspace must be a dense uint8 tensor")
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
         mk_paged_attention(a, s)
     return out
 
@@ -581,6 +606,16 @@ def _scale(scale):
     return float(scale)
 
 
+def _dense_rows(name, t, dtype, rows, width=None):
+    """Address and row stride of a [rows][width] tensor with dense rows."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or (width is not None and t.shape[1] != width):
+        _refuse(f"{name} must be {dtype} [{rows}][{'n' if width is None else width}], not {t.dtype} {list(t.shape)}")
+    row, one = t.stride()
+    if one != 1 and t.shape[1] > 1:
+        _refuse(f"{name} must have dense rows")
+    return t.data_ptr(), row if rows > 1 else t.shape[1]
+
+
 def process_logits(logits, history=None, history_lens=None, prompt_lens=None, repetition=None, frequency=None,
                    presence=None, bias=None, mask=None, out=None, next_tokens=None, status=None, stream=None):
     """Penalties for repeated tokens, biases and a grammar's mask on logits, and the choice (mk_process_logits).
@@ -591,50 +626,45 @@ def process_logits(logits, history=None, history_lens=None, prompt_lens=None, re
     bit set for each allowed id.  Returns (out fp32 [rows][vocab], next_tokens int32 [rows]): the given tensors, or new
     ones; ``out`` may be ``logits`` itself.  A row in which nothing is left gets token -1."""
     import torch
-    if logits.dim() != 2 or logits.dtype not in _dtypes() or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        _refuse("logits must be fp32, bf16 or fp16 [rows][vocab] with dense rows")
+    device, i32, f32 = logits.device, torch.int32, torch.float32
+    indptr, ids, values = bias if bias is not None else (None, None, None)
+    _on(device, history, history_lens, prompt_lens, repetition, frequency, presence, indptr, ids, values, mask, out,
+        next_tokens, status)
+    dtype = _dtypes().get(logits.dtype)
+    if dtype is None or logits.dim() != 2:
+        _refuse("logits must be fp32, bf16 or fp16 [rows][vocab]")
     R, V = logits.shape
     a = mk_logits_args()
-    a.rows, a.vocab, a.dtype, a.logits = R, V, _dtypes()[logits.dtype], _ptr(logits)
-    a.logits_stride = logits.stride(0) if R > 1 else V
-    indptr, ids, values = bias if bias is not None else (None, None, None)
-    _on(logits.device, history=history, history_lens=history_lens, prompt_lens=prompt_lens, repetition=repetition,
-        frequency=frequency, presence=presence, indptr=indptr, ids=ids, values=values, mask=mask, out=out,
-        next_tokens=next_tokens, status=status)
+    a.rows, a.vocab, a.dtype = R, V, dtype
+    a.logits, a.logits_stride = _dense_rows("logits", logits, logits.dtype, R, V)
     if history is not None:
-        if (history.dtype != torch.int32 or history.dim() != 2 or history.shape[0] != R or
-                (history.shape[1] > 1 and history.stride(1) != 1)):
-            _refuse("history must be int32 [rows][n] with dense rows")
+        a.history, a.history_stride = _dense_rows("history", history, i32, R)
         a.history_width = history.shape[1]
-        a.history_stride = history.stride(0) if R > 1 else history.shape[1]
-        a.history = _ptr(history) if history.shape[1] else 0
-    if a.history:
-        a.history_lens = _array("history_lens", history_lens, torch.int32, R)
-        a.prompt_lens = _array("prompt_lens", prompt_lens, torch.int32, R)
-        a.repetition = _array("repetition", repetition, torch.float32, R)
-        a.frequency = _array("frequency", frequency, torch.float32, R)
-        a.presence = _array("presence", presence, torch.float32, R)
-    elif history is None and any(t is not None for t in (history_lens, prompt_lens, repetition, frequency, presence)):
+        lens, prompts = _array("history_lens", history_lens, i32, R), _array("prompt_lens", prompt_lens, i32, R)
+        rep, freq = _array("repetition", repetition, f32, R), _array("frequency", frequency, f32, R)
+        pres = _array("presence", presence, f32, R)
+        if a.history:  # (a history without columns has no address)
+            a.history_lens, a.prompt_lens, a.repetition, a.frequency, a.presence = lens, prompts, rep, freq, pres
+    elif not (history_lens is prompt_lens is repetition is frequency is presence is None):
         _refuse("penalties and history lengths need a history")
-    if bias is not None and ids.numel():
-        a.bias_count = ids.numel()
-        a.bias_indptr = _array("bias indptr", indptr, torch.int32, R + 1)
-        a.bias_ids = _array("bias ids", ids, torch.int32, a.bias_count)
-        a.bias_values = _array("bias values", values, torch.float32, a.bias_count)
+    if bias is not None:
+        n = ids.numel()
+        addresses = _array("bias indptr", indptr, i32, R + 1), _array("bias ids", ids, i32, n), _array(
+            "bias values", values, f32, n)
+        if n:
+            a.bias_indptr, a.bias_ids, a.bias_values = addresses
+            a.bias_count = n
     if mask is not None:
-        if (mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[0] not in (1, R) or
-                mask.shape[1] != (V + 31) // 32 or (mask.shape[1] > 1 and mask.stride(1) != 1)):
-            _refuse("mask must be int32 [rows or 1][(vocab + 31) // 32] with dense rows")
-        a.mask, a.mask_stride = _ptr(mask), mask.stride(0) if mask.shape[0] > 1 else 0
-    a.status = _array("status", status, torch.int32, 1)
-    with _launch_on(logits.device, stream) as s:
+        rows = mask.shape[0] if mask.dim() == 2 and mask.shape[0] == 1 else R
+        a.mask, stride = _dense_rows("mask", mask, i32, rows, (V + 31) // 32)
+        a.mask_stride = stride if rows > 1 else 0
+    a.status = _array("status", status, i32, 1)
+    with _launch_on(device, stream) as s:
         if out is None:
-            out = torch.empty((R, V), dtype=torch.float32, device=logits.device)
+            out = torch.empty((R, V), dtype=f32, device=device)
         if next_tokens is None:
-            next_tokens = torch.empty(R, dtype=torch.int32, device=logits.device)
-        if out.dtype != torch.float32 or out.shape != logits.shape or (V > 1 and out.stride(1) != 1):
-            _refuse("out must be fp32 [rows][vocab] with dense rows")
-        a.out, a.out_stride = _ptr(out), out.stride(0) if R > 1 else V
-        a.next_tokens = _array("next_tokens", next_tokens, torch.int32, R)
+            next_tokens = torch.empty(R, dtype=i32, device=device)
+        a.out, a.out_stride = _dense_rows("out", out, f32, R, V)
+        a.next_tokens = _array("next_tokens", next_tokens, i32, R)
         mk_process_logits(a, s)
     return out, next_tokens

@@ -212,10 +212,10 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
 
 template <class T, bool VEC>
 mk_status launch(const mk_logits_args& a, cudaStream_t s, std::string& err) {
-  auto kernel = logits_kernel<T, VEC>;
   const int smem = kTile * (a.bias_indptr ? 8 : 4);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTile * 8);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  Device dev;
+  cudaError_t e = current_device(dev);
+  if (e == cudaSuccess) e = allow<logits_kernel<T, VEC>>(dev, kTile * 8, true);
   if (e != cudaSuccess) return cuda_result(e, "mk_process_logits attributes", err);
   int cluster = 1;
   while (cluster < kMaxCluster && (a.vocab + cluster - 1) / cluster > 2048 && a.rows * cluster < 512) cluster *= 2;
@@ -232,7 +232,7 @@ mk_status launch(const mk_logits_args& a, cudaStream_t s, std::string& err) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_result(cudaLaunchKernelEx(&cfg, kernel, a, per_block), "mk_process_logits launch", err);
+  return cuda_result(cudaLaunchKernelEx(&cfg, logits_kernel<T, VEC>, a, per_block), "mk_process_logits launch", err);
 }
 
 template <class T>

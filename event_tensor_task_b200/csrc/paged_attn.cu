@@ -20,6 +20,7 @@
 //    tensor pipe is nearly idle either way.  With G <= 8 the spare rows carry
 //    what rounding takes off the probabilities (value and remainder), above 8
 //    the remainders take a second MMA: the sum sees ~16 bits of p.
+#include <algorithm>
 #include <cmath>
 
 #include "serve.cuh"
@@ -37,8 +38,8 @@ template <int D>
 struct Shape {
   static constexpr int kPiece = kKeys * D * 2 * 2;  // bytes of a warp's keys and values
   static constexpr int kStages = D == 64 ? 4 : 3;
-  static constexpr int kBlocksPerSm = 2;
-  static constexpr int kMerge = 2 * kRows * D * 4;  // two output tiles in fp32
+  static constexpr int kBlocksPerSm = D == 64 ? 3 : 2;
+  static constexpr int kMerge = kRows * D * 4;       // two half output tiles in fp32
   static constexpr int kSmem = kWarps * kStages * kPiece + kMerge;
   static constexpr int kPartial = 2 * kRows + kRows * D;  // floats: m, l, O
 };
@@ -380,67 +381,69 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
       if (FULL) sum1 += part_l[w][quad + 8] * exp2f(part_m[w][quad + 8] - top1);
     }
     const float f0 = exp2f(m0 - top0), f1 = FULL ? exp2f(m1 - top1) : 0.f;
-    float* buf = merge + (warp & 1) * kRows * D;
-    if (warp >= 2) {
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        *reinterpret_cast<float2*>(buf + quad * D + 8 * k + 2 * sub) = make_float2(o[k][0] * f0, o[k][1] * f0);
-        if (FULL)
-          *reinterpret_cast<float2*>(buf + (quad + 8) * D + 8 * k + 2 * sub) = make_float2(o[k][2] * f1, o[k][3] * f1);
-      }
-    }
-    __syncthreads();
-    if (warp < 2) {
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        float2* p = reinterpret_cast<float2*>(buf + quad * D + 8 * k + 2 * sub);
-        o[k][0] = o[k][0] * f0 + p->x;
-        o[k][1] = o[k][1] * f0 + p->y;
-        if (warp == 1) *p = make_float2(o[k][0], o[k][1]);
-        if (FULL) {
-          p = reinterpret_cast<float2*>(buf + (quad + 8) * D + 8 * k + 2 * sub);
-          o[k][2] = o[k][2] * f1 + p->x;
-          o[k][3] = o[k][3] * f1 + p->y;
-          if (warp == 1) *p = make_float2(o[k][2], o[k][3]);
-        }
-      }
-    }
-    __syncthreads();
+    // outputs add up two by two through shared memory: all of the 8 rows at once, or 16 rows in two halves of D
+    constexpr int ROWS = FULL ? 16 : 8, PARTS = FULL ? 2 : 1, W = D / PARTS, KN = W / 8;
+    float* buf = merge + (warp & 1) * ROWS * W;
+    const float* other = merge + ROWS * W;
     const bool whole = n_here == use.ntile;
-    if (warp == 0) {
-      const float* other = merge + kRows * D;
-      if (whole) {
-        const float i0 = 1.f / sum0, i1 = FULL ? 1.f / sum1 : 0.f;
-        T* row0 = static_cast<T*>(P.a.out) + use.b * P.a.o_row_stride + (first_head + quad) * P.a.o_head_stride;
-        T* row1 = row0 + 8 * P.a.o_head_stride;
+    float* part = P.partial + ((long long)blockIdx.x * 2 + slot) * S::kPartial;
+    T* row0 = static_cast<T*>(P.a.out) + use.b * P.a.o_row_stride + (first_head + quad) * P.a.o_head_stride;
+    T* row1 = row0 + 8 * P.a.o_head_stride;
+    const float i0 = 1.f / sum0, i1 = FULL ? 1.f / sum1 : 0.f;
+    if (warp == 0 && sub == 0 && !whole) {
+      part[quad] = top0;
+      part[kRows + quad] = sum0;
+      if (FULL) {
+        part[quad + 8] = top1;
+        part[kRows + quad + 8] = sum1;
+      }
+    }
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const float2 p = *reinterpret_cast<const float2*>(other + quad * D + 8 * k + 2 * sub);
-          if (quad < heads)
-            *reinterpret_cast<uint32_t*>(row0 + 8 * k + 2 * sub) = Elem<T>::pack((o[k][0] + p.x) * i0, (o[k][1] + p.y) * i0);
-          if (FULL && quad + 8 < heads) {
-            const float2 r = *reinterpret_cast<const float2*>(other + (quad + 8) * D + 8 * k + 2 * sub);
-            *reinterpret_cast<uint32_t*>(row1 + 8 * k + 2 * sub) = Elem<T>::pack((o[k][2] + r.x) * i1, (o[k][3] + r.y) * i1);
+    for (int h = 0; h < PARTS; ++h) {
+      if (h) __syncthreads();
+      if (warp >= 2) {
+#pragma unroll
+        for (int k = 0; k < KN; ++k) {
+          const float(&x)[4] = o[h * KN + k];
+          *reinterpret_cast<float2*>(buf + quad * W + 8 * k + 2 * sub) = make_float2(x[0] * f0, x[1] * f0);
+          if (FULL) *reinterpret_cast<float2*>(buf + (quad + 8) * W + 8 * k + 2 * sub) = make_float2(x[2] * f1, x[3] * f1);
+        }
+      }
+      __syncthreads();
+      if (warp < 2) {
+#pragma unroll
+        for (int k = 0; k < KN; ++k) {
+          float(&x)[4] = o[h * KN + k];
+          float2* p = reinterpret_cast<float2*>(buf + quad * W + 8 * k + 2 * sub);
+          x[0] = x[0] * f0 + p->x;
+          x[1] = x[1] * f0 + p->y;
+          if (warp == 1) *p = make_float2(x[0], x[1]);
+          if (FULL) {
+            p = reinterpret_cast<float2*>(buf + (quad + 8) * W + 8 * k + 2 * sub);
+            x[2] = x[2] * f1 + p->x;
+            x[3] = x[3] * f1 + p->y;
+            if (warp == 1) *p = make_float2(x[2], x[3]);
           }
         }
-      } else {
-        float* part = P.partial + ((long long)blockIdx.x * 2 + slot) * S::kPartial;
-        if (sub == 0) {
-          part[quad] = top0;
-          part[kRows + quad] = sum0;
-          if (FULL) {
-            part[quad + 8] = top1;
-            part[kRows + quad + 8] = sum1;
-          }
-        }
+      }
+      __syncthreads();
+      if (warp == 0) {
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const float2 p = *reinterpret_cast<const float2*>(other + quad * D + 8 * k + 2 * sub);
-          *reinterpret_cast<float2*>(part + 2 * kRows + quad * D + 8 * k + 2 * sub) = make_float2(o[k][0] + p.x, o[k][1] + p.y);
+        for (int k = 0; k < KN; ++k) {
+          const int col = h * W + 8 * k + 2 * sub;
+          const float(&x)[4] = o[h * KN + k];
+          float2 y0 = *reinterpret_cast<const float2*>(other + quad * W + 8 * k + 2 * sub), y1 = make_float2(0.f, 0.f);
+          y0 = make_float2(x[0] + y0.x, x[1] + y0.y);
           if (FULL) {
-            const float2 r = *reinterpret_cast<const float2*>(other + (quad + 8) * D + 8 * k + 2 * sub);
-            *reinterpret_cast<float2*>(part + 2 * kRows + (quad + 8) * D + 8 * k + 2 * sub) =
-                make_float2(o[k][2] + r.x, o[k][3] + r.y);
+            y1 = *reinterpret_cast<const float2*>(other + (quad + 8) * W + 8 * k + 2 * sub);
+            y1 = make_float2(x[2] + y1.x, x[3] + y1.y);
+          }
+          if (whole) {
+            if (quad < heads) *reinterpret_cast<uint32_t*>(row0 + col) = Elem<T>::pack(y0.x * i0, y0.y * i0);
+            if (FULL && quad + 8 < heads) *reinterpret_cast<uint32_t*>(row1 + col) = Elem<T>::pack(y1.x * i1, y1.y * i1);
+          } else {
+            *reinterpret_cast<float2*>(part + 2 * kRows + quad * D + col) = y0;
+            if (FULL) *reinterpret_cast<float2*>(part + 2 * kRows + (quad + 8) * D + col) = y1;
           }
         }
       }
@@ -488,18 +491,24 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ PagedPa
   out[d] = static_cast<T>(o / l);
 }
 
-template <class T, int D>
-mk_status launch(const PagedParams& P, cudaStream_t s, std::string& err) {
+template <class T, int D, bool FULL>
+mk_status launch(PagedParams& P, cudaStream_t s, std::string& err) {
   using S = Shape<D>;
-  const bool full = P.group > 8;
-  auto kernel = full ? paged_kernel<T, D, true> : paged_kernel<T, D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  Device dev;
+  cudaError_t e = current_device(dev);
+  if (e == cudaSuccess) e = allow<paged_kernel<T, D, FULL>>(dev, S::kSmem);
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention attributes", err);
-  kernel<<<P.n_cta, kThreads, S::kSmem, s>>>(P);
+  P.n_cta = std::min(kMaxCtas, dev.sms * S::kBlocksPerSm);
+  paged_kernel<T, D, FULL><<<P.n_cta, kThreads, S::kSmem, s>>>(P);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention launch", err);
   join_kernel<T, D><<<dim3(P.a.n_q_heads, P.a.batch), D, 0, s>>>(P);
   return cuda_result(cudaGetLastError(), "mk_paged_attention join launch", err);
+}
+template <class T>
+mk_status pick(PagedParams& P, cudaStream_t s, std::string& err) {
+  if (P.a.pages.head_dim == 64) return P.group > 8 ? launch<T, 64, true>(P, s, err) : launch<T, 64, false>(P, s, err);
+  return P.group > 8 ? launch<T, 128, true>(P, s, err) : launch<T, 128, false>(P, s, err);
 }
 
 }  // namespace
@@ -516,16 +525,8 @@ mk_status launch_paged(const mk_paged_attn_args& a, void* stream, std::string& e
   const float scale = a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)a.pages.head_dim);
   P.scale_log2 = scale * 1.4426950408889634f;
   P.partial = static_cast<float*>(a.workspace);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention device query", err);
-  const int D = a.pages.head_dim;
-  P.n_cta = std::min(kMaxCtas, sms * (D == 64 ? Shape<64>::kBlocksPerSm : Shape<128>::kBlocksPerSm));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.pages.dtype == MK_DTYPE_BF16)
-    return D == 64 ? launch<__nv_bfloat16, 64>(P, s, err) : launch<__nv_bfloat16, 128>(P, s, err);
-  return D == 64 ? launch<__half, 64>(P, s, err) : launch<__half, 128>(P, s, err);
+  return a.pages.dtype == MK_DTYPE_BF16 ? pick<__nv_bfloat16>(P, s, err) : pick<__half>(P, s, err);
 }
 
 }  // namespace mk

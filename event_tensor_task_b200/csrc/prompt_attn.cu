@@ -535,10 +535,11 @@ bool encode(CUtensorMap* map, int dtype, const void* p, int rank, const long lon
 
 template <class T, int D>
 mk_status launch(const PromptParams& P, cudaStream_t s, std::string& err) {
-  auto kernel = prompt_kernel<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+  Device dev;
+  cudaError_t e = current_device(dev);
+  if (e == cudaSuccess) e = allow<prompt_kernel<T, D>>(dev, Shape<D>::kSmem);
   if (e != cudaSuccess) return cuda_result(e, "mk_prompt_attention attributes", err);
-  kernel<<<P.pairs * P.a.pages.n_kv_heads, kThreads, Shape<D>::kSmem, s>>>(P);
+  prompt_kernel<T, D><<<P.pairs * P.a.pages.n_kv_heads, kThreads, Shape<D>::kSmem, s>>>(P);
   return cuda_result(cudaGetLastError(), "mk_prompt_attention launch", err);
 }
 

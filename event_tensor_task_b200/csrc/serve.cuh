@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <string>
 
 #include "device.cuh"
@@ -50,6 +51,35 @@ __device__ __forceinline__ int page_of(const mk_kv_pages& P, int b, int page_ind
     return -1;
   }
   return page;
+}
+
+// What a launch needs of the current device: its number and SM count (asked for once per device and process).
+struct Device {
+  int id = 0, sms = 0;
+};
+inline cudaError_t current_device(Device& d) {
+  static std::atomic<int> sms[64];
+  cudaError_t e = cudaGetDevice(&d.id);
+  if (e != cudaSuccess) return e;
+  const int slot = d.id & 63;
+  d.sms = d.id < 64 ? sms[slot].load(std::memory_order_relaxed) : 0;
+  if (d.sms == 0) {
+    e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.id);
+    if (e == cudaSuccess && d.id < 64) sms[slot].store(d.sms, std::memory_order_relaxed);
+  }
+  return e;
+}
+
+// A kernel's opt-in shared memory (and, where asked, clusters above 8 blocks), set once per device.
+template <auto Kernel>
+cudaError_t allow(const Device& d, int smem, bool large_clusters = false) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = d.id < 64 ? 1ull << d.id : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && large_clusters) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 inline mk_status cuda_result(cudaError_t e, const char* what, std::string& err) {

@@ -143,21 +143,29 @@ def test_tensor_calls_refuse_what_the_struct_cannot_show():
             call()
         assert e.value.status == INVALID
     # the helpers behind them
+    def fill(*a):
+        p = mk.mk_kv_pages()
+        mk._pages(p, *a)
+        return p
+
+    for bad in ((kv, kv.transpose(1, 2).contiguous().transpose(1, 2), i, 2),  # other strides
+                (kv, kv, i.long(), 2), (kv.float(), kv.float(), i, 2), (kv, kv, i, 3), (kv[0], kv[0], i, 2),
+                (kv, kv, i.T.contiguous().T, 2), (kv.transpose(2, 3), kv.transpose(2, 3), i, 2)):
+        with pytest.raises(mk.MkError):
+            fill(*bad)
     with pytest.raises(mk.MkError):
-        mk._pages(kv, kv.transpose(1, 2).contiguous().transpose(1, 2), i, 2)  # other strides
-    with pytest.raises(mk.MkError):
-        mk._pages(kv, kv, i.long(), 2)
-    with pytest.raises(mk.MkError):
-        mk._pages(kv.float(), kv.float(), i, 2)
-    with pytest.raises(mk.MkError):
-        mk._rows("q", q.transpose(1, 2), (2, 64, 4), q.dtype)
+        mk._rows("q", q.transpose(1, 2), q.transpose(1, 2).shape, q.dtype)
     with pytest.raises(mk.MkError):
         mk._array("lens", i[:, 0], torch.int32, 2)  # not dense
     with pytest.raises(mk.MkError):
+        mk._dense_rows("mask", i, torch.int32, 2, 4)
+    with pytest.raises(mk.MkError):
         mk._scale(0.0)
-    p = mk._pages(kv, kv, i, 2)
+    p = fill(kv, kv, i, 2)
     assert (p.n_pages, p.n_kv_heads, p.page_size, p.head_dim, p.table_width, p.table_stride) == (3, 2, 16, 64, 3, 3)
     assert (p.page_stride, p.head_stride, p.row_stride) == (2048, 1024, 64)
+    p = fill(kv[:1], kv[1:2], i, 2)
+    assert (p.page_stride, p.head_stride, p.row_stride) == (0, 1024, 64)  # (one page: its stride is not used)
 
 
 # ------------------------------------------------------------------------------------------------ the oracle's pins
