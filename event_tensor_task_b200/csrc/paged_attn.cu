@@ -12,8 +12,8 @@
 //    sequences' lengths; a block's share begins and ends inside a pair, so it
 //    leaves at most two partial results, and a second kernel joins them;
 //  - a warp owns 16 keys of each unit and runs alone: its own ring of stages
-//    in shared memory (cp.async, 16 bytes a lane, rows gathered through the
-//    page table, zeros past the end), its own running maximum, sum and output
+//    in shared memory (TMA boxes of 16 rows out of the pages, or rows gathered
+//    by cp.async where pages are no multiple of 16 rows), its own running maximum, sum and output
 //    in registers; the block's four warps meet only where a pair ends;
 //  - the products are warp MMAs (m16n8k16, the group's heads as rows): at most
 //    16 rows make a tile too small for tcgen05, whose M is 64 or more, and the
@@ -32,6 +32,7 @@ constexpr int kThreads = 128, kWarps = 4;
 constexpr int kKeys = 16;               // keys of a warp's piece of a unit
 constexpr int kUnit = kKeys * kWarps;   // keys of a unit
 constexpr int kRows = 16;               // query heads of a tile
+constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of a wait
 constexpr int kMaxCtas = 640;           // the workspace holds two partials of each
 
 template <int D>
@@ -40,11 +41,12 @@ struct Shape {
   static constexpr int kStages = D == 64 ? 4 : 3;
   static constexpr int kBlocksPerSm = D == 64 ? 3 : 2;
   static constexpr int kMerge = kRows * D * 4;       // two half output tiles in fp32
-  static constexpr int kSmem = kWarps * kStages * kPiece + kMerge;
+  static constexpr int kSmem = kWarps * kStages * kPiece + kMerge + 1024;
   static constexpr int kPartial = 2 * kRows + kRows * D;  // floats: m, l, O
 };
 
 struct PagedParams {
+  CUtensorMap tk, tv;  // (page_size a multiple of 16)
   mk_paged_attn_args a;
   float scale_log2;
   int group, tiles;    // G; tiles of 16 heads per kv head
@@ -162,12 +164,16 @@ __device__ __forceinline__ long long row_offset(const PagedParams& P, const Walk
   return page * g.page_stride + (long long)(w.h / P.tiles) * g.head_stride + row * g.row_stride;
 }
 
-// FULL: 9 to 16 heads in the tile (both halves of the MMA's rows are heads)
-template <class T, int D, bool FULL>
+// FULL: 9 to 16 heads in the tile (both halves of the MMA's rows are heads).
+// TMA: page_size is a multiple of 16, so a warp's 16 keys lie in one page and
+// come as boxes of 64 dimensions x 16 rows; else the rows are gathered one by one.
+template <class T, int D, bool FULL, bool TMA>
 __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel(const __grid_constant__ PagedParams P) {
   using S = Shape<D>;
   constexpr int CH = D / 8;  // 16-byte chunks of a row
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);  // (the swizzle goes by address)
+  __shared__ uint64_t landed[kWarps][S::kStages];
   __shared__ long long scratch[kThreads + 1];
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -175,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
   float* merge = reinterpret_cast<float*>(smem + kWarps * S::kStages * S::kPiece);
   const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kPiece;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int per;
   const long long total = scan_units<kThreads>(P, scratch, per);
   const long long u0 = total * blockIdx.x / P.n_cta, u1 = total * (blockIdx.x + 1) / P.n_cta;
@@ -202,32 +209,72 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
   Walk use = load;
   const int n_units = (int)(u1 - u0);
 
-  // the lane's key of the piece that is loaded next; its offset is looked up one unit ahead
-  const int my_key = warp * kKeys + (lane & 15);
-  long long off = row_offset(P, load, load.tile * kUnit + my_key);
-  const char* kbase = static_cast<const char*>(P.a.pages.k);
-  const char* vbase = static_cast<const char*>(P.a.pages.v);
+  // The piece that is loaded next, its page looked up one unit ahead.  A piece holds its keys' 16 rows, then its
+  // values', each as halves of 64 dimensions: 128 bytes a row, 16-byte chunks swizzled by the row's low three bits.
+  constexpr int kHalf = kKeys * 128, kRowsOfKeys = kKeys * D * 2;
+  const int my_key = warp * kKeys + (TMA ? 0 : (lane & 15));
+  long long off = 0;
+  int page = 0, row = 0;
+  auto look_up = [&]() {
+    const int t = load.tile * kUnit + my_key;
+    if (TMA) {
+      const unsigned ps = P.a.pages.page_size;
+      page = t < load.len ? page_of(P.a.pages, load.b, (unsigned)t / ps, P.a.status) : -1;
+      row = (unsigned)t % ps;
+    } else {
+      off = row_offset(P, load, t);
+    }
+  };
+  look_up();
   int issued = 0;
+  bool lost = false;  // a wait has run out: the rest is computed without waiting, the status word tells
   auto issue = [&]() {
     if (issued < n_units) {
-      const uint32_t st = ring + (issued % S::kStages) * S::kPiece;
+      const int stage = issued % S::kStages;
+      const uint32_t st = ring + stage * S::kPiece;
+      if (TMA) {
+        if (lane == 0) {
+          unsigned char* dst = smem + (warp * S::kStages + stage) * S::kPiece;
+          const int head = load.h / P.tiles, p = page < 0 ? P.a.pages.n_pages : page;  // (no such page: zeros)
+          mbar_arrive_expect_tx(&landed[warp][stage], S::kPiece);
 #pragma unroll
-      for (int i = 0; i < kKeys * CH / 32; ++i) {
-        const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-        const long long o = __shfl_sync(~0u, off, r);
-        const uint32_t d = st + r * (D * 2) + ((c ^ (r & 7)) << 4);
-        const long long byte = (o < 0 ? 0 : o + c * 8) * 2;
-        cp16(d, kbase + byte, o >= 0);
-        cp16(d + kKeys * D * 2, vbase + byte, o >= 0);
+          for (int h = 0; h < D / 64; ++h) {
+            tma_load_4d(dst + h * kHalf, &P.tk, 64 * h, row, head, p, &landed[warp][stage]);
+            tma_load_4d(dst + kRowsOfKeys + h * kHalf, &P.tv, 64 * h, row, head, p, &landed[warp][stage]);
+          }
+        }
+        __syncwarp();
+      } else {
+        const char* kbase = static_cast<const char*>(P.a.pages.k);
+        const char* vbase = static_cast<const char*>(P.a.pages.v);
+#pragma unroll
+        for (int i = 0; i < kKeys * CH / 32; ++i) {
+          const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+          const long long o = __shfl_sync(~0u, off, r);
+          const uint32_t d = st + (c / 8) * kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4);
+          const long long byte = (o + c * 8) * 2;
+          cp16(d, o < 0 ? P.a.q : kbase + byte, o >= 0);  // (no such row: zeros, nothing is read)
+          cp16(d + kRowsOfKeys, o < 0 ? P.a.q : vbase + byte, o >= 0);
+        }
       }
       ++issued;
       if (issued < n_units) {
         load.next(P);
-        off = row_offset(P, load, load.tile * kUnit + my_key);
+        look_up();
       }
     }
-    cp_commit();
+    if (!TMA) cp_commit();
   };
+  if (TMA) {
+    if (lane == 0) {
+      for (int i = 0; i < S::kStages; ++i) mbar_init(&landed[warp][i], 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+  }
+  // the lane's place in the 8 x 8 matrices of a 16 x 16 block: row and chunk, the swizzle applied; chunk 2k is ^ (k << 5)
+  const int kr = (lane & 7) + ((lane >> 4) << 3), vr = lane & 15;
+  const uint32_t kat = kr * 128 + ((((lane >> 3) & 1) ^ (kr & 7)) << 4), vat = kRowsOfKeys + vr * 128 + (((lane >> 4) ^ (vr & 7)) << 4);
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) issue();
 
@@ -261,20 +308,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
 
     for (int i = 0; i < n_here; ++i, ++u) {
       issue();
-      cp_wait<S::kStages - 1>();
-      __syncwarp();
-      const uint32_t kt = ring + (u % S::kStages) * S::kPiece, vt = kt + kKeys * D * 2;
-      float s[2][4] = {};
-      {
-        // matrices: (keys 0-7, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 0-7), (keys 8-15, dims 8-15)
-        const int r = (lane & 7) + ((lane >> 4) << 3), c1 = (lane >> 3) & 1;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          ldsm4(b, kt + r * (D * 2) + (((2 * k + c1) ^ (r & 7)) << 4));
-          mma16816<T>(s[0], q[k], b[0], b[1]);
-          mma16816<T>(s[1], q[k], b[2], b[3]);
+      const uint32_t at = ring + (u % S::kStages) * S::kPiece;
+      if (TMA) {
+        uint64_t* bar = &landed[warp][u % S::kStages];
+        const uint32_t parity = (u / S::kStages) & 1;
+        if (!lost && !mbar_try(bar, parity)) {
+          const unsigned long long t0 = global_ns();
+          while (!mbar_try(bar, parity)) {
+            if (global_ns() - t0 > kWaitNs) {
+              if (P.a.status) *P.a.status = MK_ERR_DEVICE_TIMEOUT;
+              lost = true;
+              break;
+            }
+          }
+          lost = __any_sync(~0u, lost);
         }
+      } else {
+        cp_wait<S::kStages - 1>();
+      }
+      __syncwarp();
+      float s[2][4] = {};
+      // matrices: (keys 0-7, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 0-7), (keys 8-15, dims 8-15)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldsm4(b, (at + (k / 4) * kHalf + kat) ^ ((k % 4) << 5));
+        mma16816<T>(s[0], q[k], b[0], b[1]);
+        mma16816<T>(s[1], q[k], b[2], b[3]);
       }
       const int left = use.len - (use.tile + i) * kUnit - warp * kKeys;  // keys of the piece that exist
 #pragma unroll
@@ -328,19 +388,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
           hi[2 * t + 1] = rest0;  // rows 8 to 15: the remainders of rows 0 to 7
         }
       }
-      {
-        // transposed: (keys 0-7, dims 0-7), (keys 8-15, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 8-15)
-        const int r = lane & 15, c1 = lane >> 4;
+      // A row behind the last key may hold anything, NaN too, and has probability 0: it is left out of the product.
+      // (Gathered rows behind the last key are zeros already.)
+      const bool ragged = TMA && left < kKeys;
+      const uint32_t live0 = (2 * sub < left ? 0xffffu : 0u) | (2 * sub + 1 < left ? 0xffff0000u : 0u);
+      const uint32_t live1 = (2 * sub + 8 < left ? 0xffffu : 0u) | (2 * sub + 9 < left ? 0xffff0000u : 0u);
+      // transposed: (keys 0-7, dims 0-7), (keys 8-15, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 8-15)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          ldsm4_trans(b, vt + r * (D * 2) + (((2 * k + c1) ^ (r & 7)) << 4));
-          mma16816<T>(o[2 * k], hi, b[0], b[1]);
-          mma16816<T>(o[2 * k + 1], hi, b[2], b[3]);
-          if (FULL) {
-            mma16816<T>(o[2 * k], lo, b[0], b[1]);
-            mma16816<T>(o[2 * k + 1], lo, b[2], b[3]);
-          }
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldsm4_trans(b, (at + (k / 4) * kHalf + vat) ^ ((k % 4) << 5));
+        if (ragged) {
+          b[0] &= live0;
+          b[1] &= live1;
+          b[2] &= live0;
+          b[3] &= live1;
+        }
+        mma16816<T>(o[2 * k], hi, b[0], b[1]);
+        mma16816<T>(o[2 * k + 1], hi, b[2], b[3]);
+        if (FULL) {
+          mma16816<T>(o[2 * k], lo, b[0], b[1]);
+          mma16816<T>(o[2 * k + 1], lo, b[2], b[3]);
         }
       }
       __syncwarp();  // the stage is read before the next copy into it is issued
@@ -455,60 +523,123 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
   }
 }
 
-// The parts of one (sequence, query head) joined: a block of D threads, one value each.
+// The parts of one (sequence, query head) joined.  Launched while the first
+// kernel runs (programmatic dependent launch): it finds its place among the
+// shares, then waits for the parts.  Their weights are taken first, one part a
+// thread, so that the outputs' loads do not wait for one another.
+constexpr int kJoinThreads = 128;
+
 template <class T, int D>
-__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ PagedParams P) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ PagedParams P) {
   using S = Shape<D>;
-  __shared__ long long scratch[D + 1];
-  const int head = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;  // threads of a part's row, 4 values each
+  __shared__ long long scratch[kJoinThreads + 1];
+  __shared__ int where[kMaxCtas];
+  __shared__ float weight[kMaxCtas], red[kJoinThreads / 32];
+  __shared__ float4 acc[GROUPS][LANES];
+  const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   int per;
-  const long long total = scan_units<D>(P, scratch, per);
+  const long long total = scan_units<kJoinThreads>(P, scratch, per);
   T* out = static_cast<T*>(P.a.out) + b * P.a.o_row_stride + head * P.a.o_head_stride;
   const int ntile = (keys_of(P.a, b) + kUnit - 1) / kUnit;
-  if (ntile == 0) {
-    out[d] = static_cast<T>(0.f);
-    return;
-  }
   const int pairs = P.a.pages.n_kv_heads * P.tiles;
   long long at = scratch[b / per];
   for (int i = b / per * per; i < b; ++i) at += (long long)((keys_of(P.a, i) + kUnit - 1) / kUnit) * pairs;
   const int in_group = head % P.group, row = in_group % kRows;
   const long long p0 = at + (long long)((head / P.group) * P.tiles + in_group / kRows) * ntile, p1 = p0 + ntile;
   // block c's share is [total c / n, total (c + 1) / n): unit u is in share ((u + 1) n - 1) / total
-  const int c0 = (int)(((p0 + 1) * P.n_cta - 1) / total), c1 = (int)((p1 * P.n_cta - 1) / total);
-  if (c0 == c1) return;  // one block had it all and wrote it
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const long long u0 = total * c / P.n_cta, u1 = total * (c + 1) / P.n_cta;
-    if (u0 >= u1) continue;
-    const float* part = P.partial + ((long long)c * 2 + (u0 < p0 ? 1 : 0)) * S::kPartial;
-    const float pm = part[row], pl = part[kRows + row], po = part[2 * kRows + row * D + d];
-    const float top = fmaxf(m, pm), f = exp2f(m - top), g = exp2f(pm - top);
-    l = l * f + pl * g;
-    o = o * f + po * g;
-    m = top;
+  const int c0 = ntile ? (int)(((p0 + 1) * P.n_cta - 1) / total) : 0, c1 = ntile ? (int)((p1 * P.n_cta - 1) / total) : 0;
+  const int n = c1 - c0 + 1;
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const long long u0 = total * (c0 + i) / P.n_cta, u1 = total * (c0 + i + 1) / P.n_cta;
+    where[i] = u0 < u1 ? (c0 + i) * 2 + (u0 < p0 ? 1 : 0) : -1;  // (an empty share has no part)
   }
-  out[d] = static_cast<T>(o / l);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (ntile == 0) {
+    if (tid < D) out[tid] = static_cast<T>(0.f);
+    return;
+  }
+  if (n == 1) return;  // one block had it all and wrote it
+  float m = -INFINITY;
+  for (int i = tid; i < n; i += kJoinThreads) {
+    weight[i] = where[i] < 0 ? -INFINITY : P.partial[(long long)where[i] * S::kPartial + row];
+    m = fmaxf(m, weight[i]);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
+  __syncthreads();
+  float l = 0.f;
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float w = exp2f(weight[i] - m);
+    weight[i] = w;
+    if (where[i] >= 0) l += w * P.partial[(long long)where[i] * S::kPartial + kRows + row];
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+  if ((tid & 31) == 0) red[tid >> 5] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w];
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int g = tid / LANES, c = tid % LANES;
+#pragma unroll 4
+  for (int i = g; i < n; i += GROUPS) {
+    if (where[i] < 0) continue;
+    const float4 v = *reinterpret_cast<const float4*>(P.partial + (long long)where[i] * S::kPartial + 2 * kRows + row * D + 4 * c);
+    const float w = weight[i];
+    o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+  }
+  acc[g][c] = o;
+  __syncthreads();
+  if (g == 0) {
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+      const float4 v = acc[i][c];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const float inv = 1.f / l;
+    *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
+  }
 }
 
-template <class T, int D, bool FULL>
+template <class T, int D, bool FULL, bool TMA>
 mk_status launch(PagedParams& P, cudaStream_t s, std::string& err) {
   using S = Shape<D>;
   Device dev;
   cudaError_t e = current_device(dev);
-  if (e == cudaSuccess) e = allow<paged_kernel<T, D, FULL>>(dev, S::kSmem);
+  if (e == cudaSuccess) e = allow<paged_kernel<T, D, FULL, TMA>>(dev, S::kSmem);
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention attributes", err);
   P.n_cta = std::min(kMaxCtas, dev.sms * S::kBlocksPerSm);
-  paged_kernel<T, D, FULL><<<P.n_cta, kThreads, S::kSmem, s>>>(P);
+  paged_kernel<T, D, FULL, TMA><<<P.n_cta, kThreads, S::kSmem, s>>>(P);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention launch", err);
-  join_kernel<T, D><<<dim3(P.a.n_q_heads, P.a.batch), D, 0, s>>>(P);
-  return cuda_result(cudaGetLastError(), "mk_paged_attention join launch", err);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P.a.n_q_heads, P.a.batch);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_result(cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P), "mk_paged_attention join launch", err);
 }
-template <class T>
+template <class T, int D>
 mk_status pick(PagedParams& P, cudaStream_t s, std::string& err) {
-  if (P.a.pages.head_dim == 64) return P.group > 8 ? launch<T, 64, true>(P, s, err) : launch<T, 64, false>(P, s, err);
-  return P.group > 8 ? launch<T, 128, true>(P, s, err) : launch<T, 128, false>(P, s, err);
+  const mk_kv_pages& g = P.a.pages;
+  if (g.page_size % kKeys == 0 && g.n_pages > 0) {
+    if (!encode_pages(&P.tk, &P.tv, g, kKeys)) {
+      err = "the driver takes no tensor map of the keys' strides";
+      return MK_ERR_UNSUPPORTED;
+    }
+    return P.group > 8 ? launch<T, D, true, true>(P, s, err) : launch<T, D, false, true>(P, s, err);
+  }
+  return P.group > 8 ? launch<T, D, true, false>(P, s, err) : launch<T, D, false, false>(P, s, err);
 }
 
 }  // namespace
@@ -526,7 +657,10 @@ mk_status launch_paged(const mk_paged_attn_args& a, void* stream, std::string& e
   P.scale_log2 = scale * 1.4426950408889634f;
   P.partial = static_cast<float*>(a.workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return a.pages.dtype == MK_DTYPE_BF16 ? pick<__nv_bfloat16>(P, s, err) : pick<__half>(P, s, err);
+  const bool wide = a.pages.head_dim == 128;
+  if (a.pages.dtype == MK_DTYPE_BF16)
+    return wide ? pick<__nv_bfloat16, 128>(P, s, err) : pick<__nv_bfloat16, 64>(P, s, err);
+  return wide ? pick<__half, 128>(P, s, err) : pick<__half, 64>(P, s, err);
 }
 
 }  // namespace mk

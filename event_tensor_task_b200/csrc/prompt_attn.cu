@@ -25,11 +25,8 @@
 // Bound: at D = 128 the two products and the exponentials take the same time
 // (128 x 128 scores: 1,024 cycles of the tensor pipe, 1,024 of the MUFU); at
 // D = 64 the exponentials take twice the products' time.
-#include <cuda.h>
-
 #include <algorithm>
 #include <cmath>
-#include <cstring>
 
 #include "serve.cuh"
 
@@ -92,14 +89,6 @@ __device__ __forceinline__ bool await(Control& c, uint64_t* bar, uint32_t parity
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
   const unsigned long long t0 = global_ns();
   while (!mbar_try(bar, parity) && global_ns() - t0 < kWaitNs) {}
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-          smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
 }
 
 // Shared-memory descriptor of an operand whose M or N is contiguous, under the
@@ -500,39 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
-// A map of 16-bit elements [dims...] with element strides (of dimension 1 on), read in boxes of 64 x box under the
-// 128-byte swizzle.  A dimension of one element has no stride of its own.
-bool encode(CUtensorMap* map, int dtype, const void* p, int rank, const long long* dims, const long long* strides,
-            const int* box) {
-  EncodeTiledFn enc = encode_tiled();
-  cuuint64_t d[4], st[3];
-  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    d[i] = (cuuint64_t)dims[i];
-    b[i] = (cuuint32_t)box[i];
-    if (i) st[i - 1] = (cuuint64_t)(dims[i] == 1 ? dims[0] : strides[i - 1]) * 2;
-  }
-  return enc && enc(map, dtype == MK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-                    const_cast<void*>(p), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <class T, int D>
 mk_status launch(const PromptParams& P, cudaStream_t s, std::string& err) {
   Device dev;
@@ -566,21 +522,16 @@ mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err)
   {
     const long long dims[3] = {D, a.n_q_heads, a.n_tokens}, strides[2] = {a.q_head_stride, a.q_row_stride};
     const int box[3] = {64, P.group, P.tokens};
-    if (!encode(&P.tq, g.dtype, a.q, 3, dims, strides, box)) {
+    if (!encode_map(&P.tq, g.dtype, a.q, 3, dims, strides, box)) {
       err = "the driver takes no tensor map of q's strides";
       return MK_ERR_UNSUPPORTED;
     }
   }
   // (no keys at all: nothing is loaded, the maps are those of q)
   P.tk = P.tv = P.tq;
-  if (g.n_pages > 0 && g.page_size > 0) {
-    const long long dims[4] = {D, g.page_size, g.n_kv_heads, g.n_pages};
-    const long long strides[3] = {g.row_stride, g.head_stride, g.page_stride};
-    const int box[4] = {64, P.box, 1, 1};
-    if (!encode(&P.tk, g.dtype, g.k, 4, dims, strides, box) || !encode(&P.tv, g.dtype, g.v, 4, dims, strides, box)) {
-      err = "the driver takes no tensor map of the keys' strides";
-      return MK_ERR_UNSUPPORTED;
-    }
+  if (g.n_pages > 0 && g.page_size > 0 && !encode_pages(&P.tk, &P.tv, g, P.box)) {
+    err = "the driver takes no tensor map of the keys' strides";
+    return MK_ERR_UNSUPPORTED;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (g.dtype == MK_DTYPE_BF16)

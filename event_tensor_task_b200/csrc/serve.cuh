@@ -1,6 +1,7 @@
 // serve.cuh — what the serving operators' kernels share: 16-bit element types,
 // the paged cache's view, the status word and launches with attributes.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -80,6 +81,47 @@ cudaError_t allow(const Device& d, int smem, bool large_clusters = false) {
   if (e == cudaSuccess && large_clusters) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+// A map of 16-bit elements [dims...] with element strides (of dimension 1 on), read in boxes of 64 x box under the
+// 128-byte swizzle.  A dimension of one element has no stride of its own.
+inline bool encode_map(CUtensorMap* map, int dtype, const void* p, int rank, const long long* dims, const long long* strides,
+            const int* box) {
+  EncodeTiledFn enc = encode_tiled();
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    if (i) st[i - 1] = (cuuint64_t)(dims[i] == 1 ? dims[0] : strides[i - 1]) * 2;
+  }
+  return enc && enc(map, dtype == MK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                    const_cast<void*>(p), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The maps of a pool's keys and values, read in boxes of 64 elements x `rows` rows of one (page, head): coordinates
+// (element, row, head, page); what lies behind a page or the pool reads as zeros.
+inline bool encode_pages(CUtensorMap* k, CUtensorMap* v, const mk_kv_pages& g, int rows) {
+  const long long dims[4] = {g.head_dim, g.page_size, g.n_kv_heads, g.n_pages};
+  const long long strides[3] = {g.row_stride, g.head_stride, g.page_stride};
+  const int box[4] = {64, rows, 1, 1};
+  return encode_map(k, g.dtype, g.k, 4, dims, strides, box) && encode_map(v, g.dtype, g.v, 4, dims, strides, box);
 }
 
 inline mk_status cuda_result(cudaError_t e, const char* what, std::string& err) {
