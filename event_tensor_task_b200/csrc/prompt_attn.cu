@@ -19,7 +19,9 @@
 //   warp 8:          one thread issues the MMAs, S = Q K^T (Q, K from shared
 //                    memory, both K-major) and O += P V (P from TMEM, V from
 //                    shared memory, its N = dimensions contiguous);
-//   warp 9:          TMA loads, K and V tiles of 128 keys in a ring.
+//   warp 9:          TMA loads, K and V tiles of 128 keys in a ring
+//                    (warps 10 and 11 fill up the warpgroup whose registers
+//                    the softmax warps take over).
 // While one tile is in its softmax, the other has the tensor pipe.
 //
 // Bound: at D = 128 the two products and the exponentials take the same time
@@ -34,7 +36,7 @@ namespace mk {
 namespace {
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // (registers move between whole warpgroups)
 constexpr int kRows = 128;   // rows of a tile, keys of a tile
 constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
 constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait
@@ -43,6 +45,7 @@ template <int D>
 struct Shape {
   static constexpr int kTile = kRows * D * 2;        // bytes of 128 rows
   static constexpr int kStages = D == 64 ? 8 : 4;    // ring of K and V tiles
+  static constexpr int kFma = D == 64 ? 4 : 2;       // of 8 exponentials, how many go over the FMA pipes
   static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024;
 };
 
@@ -144,6 +147,75 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// two fp32 values in one register pair: one instruction for both
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x of a pair on the FMA pipes, for x in [-125, 64] (smaller x as -125):
+// x = n + f with n whole and |f| <= 1/2 (Cody-Waite reduction by adding
+// 1.5 2^23), 2^f by a degree-4 polynomial, n into the exponent.  The
+// coefficients are those of the least relative error on [-1/2, 1/2] (Remez
+// exchange): 2^-18.5, far below a 16-bit probability's half step.
+__device__ __forceinline__ float2 ex2_fma(uint64_t x) {
+  float2 v = both(x);
+  x = pair(fmaxf(v.x, -125.f), fmaxf(v.y, -125.f));
+  const uint64_t magic = pair(12582912.f, 12582912.f);
+  const uint64_t t = add2(x, magic);
+  const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
+  uint64_t p = fma2(pair(0.009570102f, 0.009570102f), f, pair(0.055917859f, 0.055917859f));
+  p = fma2(p, f, pair(0.24024744f, 0.24024744f));
+  p = fma2(p, f, pair(0.69312179f, 0.69312179f));
+  p = fma2(p, f, pair(0.99999928f, 0.99999928f));
+  const float2 n = both(t), y = both(p);
+  return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(n.x) << 23)),
+                     __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(n.y) << 23)));
+}
+// p = 2^(c s - m) of the 128 scores in x, 16-bit pairs to TMEM at `dst`;
+// returns their sum.  FMA of 8 pairs go over the FMA pipes, the others over
+// the MUFU.
+template <class T, int FMA>
+__device__ __forceinline__ float exponentials(const uint32_t* x, float c, float m, uint32_t dst) {
+  const uint64_t cc = pair(c, c), mm = pair(-m, -m);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kRows; i += 32) {
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t u = fma2(pair(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])), cc, mm);
+      float2 y;
+      if ((e * FMA) / 8 != ((e + 1) * FMA) / 8) {
+        y = ex2_fma(u);
+      } else {
+        y = both(u);
+        y = make_float2(ex2(y.x), ex2(y.y));
+      }
+      sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
+      p[e] = Elem<T>::pack(y.x, y.y);
+    }
+    tmem_st16(dst + i / 2, p);
+  }
+  const float2 a = both(add2(sum[0], sum[1]));
+  return a.x + a.y;
 }
 
 // One sequence: its query rows, key rows and where they lie.
@@ -262,7 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = c.tmem;  // S0, S1 at columns 0 and 128, O0, O1 at 256 and 256 + D
 
-  if (warp == kSoftmaxWarps + 1) {
+  // registers: 2 x 128 x 208 + 128 x 80 of the 384 x 168 that the block was launched with
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == kSoftmaxWarps + 1) {
     // ---- loads
     if (n_tiles > 0) {
       if (lane == 0) {
@@ -305,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       drain(&c.q_full, 0);
       for (int i = max(0, issued - S::kStages); i < issued; ++i) drain(&c.kv_full[i % S::kStages], (i / S::kStages) & 1);
     }
-  } else if (warp == kSoftmaxWarps) {
+    } else if (warp == kSoftmaxWarps) {
     // ---- MMAs: the warp waits together, lane 0 issues
     if (n_tiles > 0) {
       constexpr uint32_t id_qk = idesc<T>(kRows, false), id_pv = idesc<T>(D, true);
@@ -382,8 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         __syncwarp();
       }
     }
+    }
   } else {
     // ---- softmax: a thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp >> 2, r = tid & 127;
     const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + 128u * t;
     const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + 256u + D * t;
@@ -402,14 +479,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       tmem_wait_ld();
       const int sub = (j % P.per_span) * kRows;
       const int live = min(limit - ((j / P.per_span) * P.span + sub), P.span - sub);  // columns the row sees
-      if (__any_sync(~0u, live < kRows)) {
+      const bool masked = __any_sync(~0u, live < kRows);
+      if (masked) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
           if (i >= live) x[i] = 0xff800000u;
       }
-      float top = __uint_as_float(x[0]);
+      float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 1; i < kRows; ++i) top = fmaxf(top, __uint_as_float(x[i]));
+      for (int i = 0; i < kRows; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          part[e] = fmaxf(fmaxf(part[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + 4 + e]));
+      float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
       top *= P.scale_log2;
       if (j == 0) {
         m = top == -INFINITY ? 0.f : top;
@@ -430,21 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           tmem_st32(to + i, o);
         }
       }
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < kRows; i += 32) {
-        uint32_t p[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float u = ex2(fmaf(__uint_as_float(x[i + 2 * e]), P.scale_log2, -m));
-          const float v = ex2(fmaf(__uint_as_float(x[i + 2 * e + 1]), P.scale_log2, -m));
-          sum[0] += u;
-          sum[1] += v;
-          p[e] = Elem<T>::pack(u, v);
-        }
-        tmem_st16(ts + i / 2, p);
-      }
-      l += sum[0] + sum[1];
+      // (a masked score's probability is an exact zero only over the MUFU)
+      l += masked ? exponentials<T, 0>(x, P.scale_log2, m, ts) : exponentials<T, S::kFma>(x, P.scale_log2, m, ts);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -3,8 +3,8 @@
 Tolerances, elementwise, with u = half a step of the 16-bit type:
  - a stored value is rounded once: u |x|;
  - attention: a score is a D-term fp32 sum, off by at most D 2^-24 times the sum of |q_i k_i|, which makes each
-   probability off by that fraction (twice: numerator and sum); the exponential adds 2^-21 and an n-key sum
-   n 2^-24; a probability rounded to the type for its product is off by u (prompt attention), as value and
+   probability off by that fraction (twice: numerator and sum); the exponential adds 2^-21 (single tokens) or
+   2^-18 (prompts: a polynomial within 2^-18.5, plus roundings), twice as well; an n-key sum n 2^-24; a probability rounded to the type for its product is off by u (prompt attention), as value and
    remainder by u^2 (single tokens).  Each is a fraction of the mean of |v| under the probabilities.  In fp16
    a probability below 2^-14 of the running maximum has a step of 2^-24: n 2^-25 max |v| more;
  - rotation: the reduced angle in [-pi, pi] is rounded to fp32 (2^-22.3) and sine and cosine are within two of
@@ -77,7 +77,7 @@ def check_attention(got, ref, dtype, n_keys, vmax, single):
     out, mag, big = ref
     d = out.shape[-1]
     u = half_step(dtype)
-    frac = 2 * (d * 2.0**-24 * big) + 2.0**-21 + n_keys * 2.0**-24 + (u * u if single else u)
+    frac = 2 * (d * 2.0**-24 * big + (2.0**-21 if single else 2.0**-18)) + n_keys * 2.0**-24 + (u * u if single else u)
     tol = u * out.abs() + frac * mag * (1 + u)
     if dtype == HF:
         tol = tol + n_keys * 2.0**-25 * vmax * (0.002 if single else 1.0)
