@@ -60,7 +60,7 @@ struct PromptParams {
 };
 
 struct Control {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2], v_tail;
   uint32_t tmem;
   int abort;
   int warp_sum[kSoftmaxWarps];
@@ -94,13 +94,22 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
   while (!mbar_try(bar, parity) && global_ns() - t0 < kWaitNs) {}
 }
 
-// Shared-memory descriptor of an operand whose M or N is contiguous, under the
-// 128-byte swizzle: 64 elements (128 bytes) a row, a row per k; 8-k groups are
-// 1024 bytes apart (stride offset 64), blocks of 64 elements 16 KB (leading
-// offset 1024).  A 16-k step is the descriptor plus 128 (2048 bytes).
-__device__ __forceinline__ uint64_t desc_mn_sw128(const void* tile) {
-  const uint64_t a = (smem_u32(tile) >> 4) & 0x3FFFull;
-  return a | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Shared-memory descriptors under the 128-byte swizzle, the upper half the
+// same for all: 8-row (8-k) groups 1024 bytes apart, version 1, 128-byte
+// swizzle.  The lower half holds the address and the leading offset, both / 16:
+// for a K-major operand (Q, K: 64 elements of k in a row) that is unused (1)
+// and a 16-k step is 32 bytes further; for V, whose rows are k and hold 64 of
+// its N dimensions, it leads to the next 64 dimensions and a 16-k step is
+// 2048 bytes further.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(const void* tile, uint32_t leading) {
+  return ((smem_u32(tile) >> 4) & 0x3FFFu) | (leading << 16);
 }
 // kind::f16 instruction descriptor: fp32 D, A and B bf16 (format 1) or fp16
 // (format 0), bit 16: B with N contiguous.
@@ -109,12 +118,19 @@ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
   const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
   return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] . B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+// D[tmem] (+)= A . B, A from shared memory or from TMEM
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(id), "r"((uint32_t)accumulate), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(id), "r"((uint32_t)accumulate), "n"(kDescHi)
       : "memory");
 }
 
@@ -314,9 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tiles[t] = seen > 0 ? full * P.per_span + (seen - full * P.span + kRows - 1) / kRows : 0;
   }
   const int n_tiles = max(tiles[0], tiles[1]);
+  // the key tile that the sequence ends inside, where this block reads it: the last one
+  int ragged = -1;
+  if (n_tiles > 0 && s.m - (((n_tiles - 1) / P.per_span) * P.span + ((n_tiles - 1) % P.per_span) * kRows) < kRows) ragged = n_tiles - 1;
 
   if (tid == 0) {
     mbar_init(&c.q_full, 1);
+    mbar_init(&c.v_tail, 1);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&c.kv_full[i], 1);
       mbar_init(&c.kv_empty[i], 1);
@@ -355,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int stage = i % S::kStages, j = i >> 1;
         if (i >= S::kStages) fine = await(c, &c.kv_empty[stage], (i / S::kStages - 1) & 1, a.status);
         if (!fine) break;
-        if (lane == 0) mbar_arrive_expect_tx(&c.kv_full[stage], S::kTile);
+        uint64_t* full = i == 2 * ragged + 1 ? &c.v_tail : &c.kv_full[stage];
+        if (lane == 0) mbar_arrive_expect_tx(full, S::kTile);
         __syncwarp();
         if (lane < boxes) {
           int page = 0, row;
@@ -371,92 +392,83 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           unsigned char* dst = ring + stage * S::kTile + lane * P.box * 128;
 #pragma unroll
           for (int h = 0; h < HALVES; ++h)
-            tma_load_4d(dst + h * (kRows * 128), (i & 1) ? &P.tv : &P.tk, 64 * h, row, kvh, page, &c.kv_full[stage]);
+            tma_load_4d(dst + h * (kRows * 128), (i & 1) ? &P.tv : &P.tk, 64 * h, row, kvh, page, full);
         }
         __syncwarp();
         issued = i + 1;
       }
       // no copy is in flight when the block leaves, even if another role has given up
       drain(&c.q_full, 0);
-      for (int i = max(0, issued - S::kStages); i < issued; ++i) drain(&c.kv_full[i % S::kStages], (i / S::kStages) & 1);
+      for (int i = max(0, issued - S::kStages); i < issued; ++i) {
+        if (i == 2 * ragged + 1) drain(&c.v_tail, 0);
+        else drain(&c.kv_full[i % S::kStages], (i / S::kStages) & 1);
+      }
     }
     } else if (warp == kSoftmaxWarps) {
-    // ---- MMAs: the warp waits together, lane 0 issues
-    if (n_tiles > 0) {
-      constexpr uint32_t id_qk = idesc<T>(kRows, false), id_pv = idesc<T>(D, true);
-      bool fine = await(c, &c.q_full, 0, a.status);
-      auto qk = [&](int t, int j) {
-        const int stage = (2 * j) % S::kStages;
-        if (lane == 0) {
+      // ---- MMAs, by one thread (elect.sync: the compiler keeps the descriptors in uniform registers)
+      if (n_tiles > 0 && elect_one()) {
+        constexpr uint32_t id_qk = idesc<T>(kRows, false), id_pv = idesc<T>(D, true);
+        const uint32_t q_lo = desc_lo(sq, 1), k_lo = desc_lo(ring, 1), v_lo = desc_lo(ring, kRows * 128 / 16);
+        auto qk = [&](int t, int stage) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const int off = (k / 4) * (kRows * 128);
-            umma_bf16(tmem + 128u * t, umma_desc_sw128(sq + t * S::kTile + off) + 2u * (k % 4),
-                      umma_desc_sw128(ring + stage * S::kTile + off) + 2u * (k % 4), id_qk, k ? 1u : 0u);
+            const uint32_t off = ((k / 4) * (kRows * 128) + (k % 4) * 32) / 16;
+            umma_ss(tmem + 128u * t, q_lo + t * (S::kTile / 16) + off, k_lo + stage * (S::kTile / 16) + off, id_qk, k != 0);
           }
           umma_commit(&c.s_full[t]);
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int t, int j) {
-        const int stage = (2 * j + 1) % S::kStages;
-        if (lane == 0) {
-          const uint64_t v = desc_mn_sw128(ring + stage * S::kTile);
+        };
+        auto pv = [&](int t, int stage, bool more) {
 #pragma unroll
           for (int k = 0; k < kRows / 16; ++k)
-            umma_ts(tmem + 256u + D * t, tmem + 128u * t + 8u * k, v + 128u * k, id_pv, (j | k) ? 1u : 0u);
+            umma_ts(tmem + 256u + D * t, tmem + 128u * t + 8u * k, v_lo + stage * (S::kTile / 16) + 128u * k, id_pv, more || k != 0);
           umma_commit(&c.pv_done[t]);
+        };
+        bool fine = await_lane(c, &c.q_full, 0, a.status) && await_lane(c, &c.kv_full[0], 0, a.status);
+        if (fine) {
+          tc_fence_after();
+          if (tiles[0] > 0) qk(0, 0);
+          if (tiles[1] > 0) qk(1, 0);
+          umma_commit(&c.kv_empty[0]);
         }
-        __syncwarp();
-      };
-      fine = fine && await(c, &c.kv_full[0], 0, a.status);
-      tc_fence_after();
-      if (fine) {
-        for (int t = 0; t < 2; ++t)
-          if (tiles[t] > 0) qk(t, 0);
-        if (lane == 0) umma_commit(&c.kv_empty[0]);
-      }
-      for (int j = 0; j < n_tiles && fine; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;
-        fine = await(c, &c.kv_full[iv % S::kStages], (iv / S::kStages) & 1, a.status);
-        if (!fine) break;
-        {
-          // rows behind the sequence's last key may hold anything, NaN too, and meet probabilities of zero: cleared
-          const int sub = (j % P.per_span) * kRows;
-          const int live = s.m - ((j / P.per_span) * P.span + sub);
-          if (live < kRows) {
-            for (int i = lane; i < (kRows - max(live, 0)) * 8 * HALVES; i += 32) {
-              const int h = i / ((kRows - max(live, 0)) * 8), r = i % ((kRows - max(live, 0)) * 8);
-              *reinterpret_cast<uint4*>(ring + (iv % S::kStages) * S::kTile + h * (kRows * 128) + max(live, 0) * 128 + r * 16) =
-                  make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < n_tiles && fine; ++j) {
+          const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % S::kStages, sk = ik % S::kStages;
+          fine = await_lane(c, &c.kv_full[sv], (iv / S::kStages) & 1, a.status);
+          if (!fine) break;
+          bool k_here = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j < tiles[t]) {
+              fine = fine && await_lane(c, &c.p_full[t], j & 1, a.status);
+              if (!fine) break;
+              tc_fence_after();
+              pv(t, sv, j > 0);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
+            if (j + 1 < tiles[t]) {
+              if (!k_here) fine = await_lane(c, &c.kv_full[sk], (ik / S::kStages) & 1, a.status);
+              if (!fine) break;
+              tc_fence_after();
+              k_here = true;
+              qk(t, sk);
+            }
           }
+          umma_commit(&c.kv_empty[sv]);
+          if (j + 1 < n_tiles) umma_commit(&c.kv_empty[sk]);
         }
-        bool k_here = false;
-        for (int t = 0; t < 2 && fine; ++t) {
-          if (j < tiles[t]) {
-            fine = await(c, &c.p_full[t], j & 1, a.status);
-            if (!fine) break;
-            tc_fence_after();
-            pv(t, j);
-          }
-          if (j + 1 < tiles[t]) {
-            if (!k_here) fine = await(c, &c.kv_full[ik % S::kStages], (ik / S::kStages) & 1, a.status);
-            if (!fine) break;
-            tc_fence_after();
-            k_here = true;
-            qk(t, j + 1);
-          }
-        }
-        if (lane == 0) {
-          umma_commit(&c.kv_empty[iv % S::kStages]);
-          if (j + 1 < n_tiles) umma_commit(&c.kv_empty[ik % S::kStages]);
-        }
-        __syncwarp();
       }
-    }
+      __syncwarp();
+    } else if (warp == kSoftmaxWarps + 2) {
+      // ---- value rows behind the sequence's last key may hold anything, NaN too, and meet probabilities of zero:
+      // cleared, before the tile counts as full
+      if (ragged >= 0 && await(c, &c.v_tail, 0, a.status)) {
+        const int live = s.m - ((ragged / P.per_span) * P.span + (ragged % P.per_span) * kRows);
+        unsigned char* v = ring + (2 * ragged + 1) % S::kStages * S::kTile + live * 128;
+        for (int i = lane; i < (kRows - live) * 8; i += 32)
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) *reinterpret_cast<uint4*>(v + h * (kRows * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.kv_full[(2 * ragged + 1) % S::kStages]);
+      }
     }
   } else {
     // ---- softmax: a thread per row
