@@ -38,6 +38,7 @@ namespace {
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // (registers move between whole warpgroups)
 constexpr int kRows = 128;   // rows of a tile, keys of a tile
+constexpr int kParts = 2;            // parts of a P tile, handed to the MMAs one by one
 constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
 constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait
 
@@ -45,7 +46,7 @@ template <int D>
 struct Shape {
   static constexpr int kTile = kRows * D * 2;        // bytes of 128 rows
   static constexpr int kStages = D == 64 ? 8 : 4;    // ring of K and V tiles
-  static constexpr int kFma = D == 64 ? 4 : 2;       // of 8 exponentials, how many go over the FMA pipes
+  static constexpr int kFma = D == 64 ? 2 : 1;       // of 8 exponentials, how many go over the FMA pipes
   static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024;
 };
 
@@ -60,7 +61,7 @@ struct PromptParams {
 };
 
 struct Control {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2], v_tail;
+  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2][kParts], pv_done[2], v_tail;
   uint32_t tmem;
   int abort;
   int warp_sum[kSoftmaxWarps];
@@ -205,11 +206,11 @@ __device__ __forceinline__ float2 ex2_fma(uint64_t x) {
   return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(n.x) << 23)),
                      __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(n.y) << 23)));
 }
-// p = 2^(c s - m) of the 128 scores in x, 16-bit pairs to TMEM at `dst`;
-// returns their sum.  FMA of 8 pairs go over the FMA pipes, the others over
+// p = 2^(c s - m) of the 128 scores in x, 16-bit pairs to TMEM at `dst`, each
+// part announced on `ready` when it is there; returns their sum.  FMA of 8 pairs go over the FMA pipes, the others over
 // the MUFU.
 template <class T, int FMA>
-__device__ __forceinline__ float exponentials(const uint32_t* x, float c, float m, uint32_t dst) {
+__device__ __forceinline__ float exponentials(const uint32_t* x, float c, float m, uint32_t dst, uint64_t* ready, int lane) {
   const uint64_t cc = pair(c, c), mm = pair(-m, -m);
   uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -229,6 +230,12 @@ __device__ __forceinline__ float exponentials(const uint32_t* x, float c, float 
       p[e] = Elem<T>::pack(y.x, y.y);
     }
     tmem_st16(dst + i / 2, p);
+    if ((i + 32) % (kRows / kParts) == 0) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready + i / (kRows / kParts));
+    }
   }
   const float2 a = both(add2(sum[0], sum[1]));
   return a.x + a.y;
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&c.s_full[t], 1);
-      mbar_init(&c.p_full[t], 4);
+      for (int i = 0; i < kParts; ++i) mbar_init(&c.p_full[t][i], 4);
       mbar_init(&c.pv_done[t], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -417,11 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           umma_commit(&c.s_full[t]);
         };
-        auto pv = [&](int t, int stage, bool more) {
+        auto pv = [&](int t, int stage, int part, bool more) {
 #pragma unroll
-          for (int k = 0; k < kRows / 16; ++k)
-            umma_ts(tmem + 256u + D * t, tmem + 128u * t + 8u * k, v_lo + stage * (S::kTile / 16) + 128u * k, id_pv, more || k != 0);
-          umma_commit(&c.pv_done[t]);
+          for (int i = 0; i < kRows / 16 / kParts; ++i) {
+            const int k = part * (kRows / 16 / kParts) + i;
+            umma_ts(tmem + 256u + D * t, tmem + 128u * t + 8u * k, v_lo + stage * (S::kTile / 16) + 128u * k, id_pv, more || i);
+          }
         };
         bool fine = await_lane(c, &c.q_full, 0, a.status) && await_lane(c, &c.kv_full[0], 0, a.status);
         if (fine) {
@@ -438,10 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (j < tiles[t]) {
-              fine = fine && await_lane(c, &c.p_full[t], j & 1, a.status);
+#pragma unroll
+              for (int i = 0; i < kParts; ++i) {
+                fine = fine && await_lane(c, &c.p_full[t][i], j & 1, a.status);
+                if (!fine) break;
+                tc_fence_after();
+                pv(t, sv, i, j > 0 || i > 0);
+              }
               if (!fine) break;
-              tc_fence_after();
-              pv(t, sv, j > 0);
+              umma_commit(&c.pv_done[t]);
             }
             if (j + 1 < tiles[t]) {
               if (!k_here) fine = await_lane(c, &c.kv_full[sk], (ik / S::kStages) & 1, a.status);
@@ -525,11 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
       }
       // (a masked score's probability is an exact zero only over the MUFU)
-      l += masked ? exponentials<T, 0>(x, P.scale_log2, m, ts) : exponentials<T, S::kFma>(x, P.scale_log2, m, ts);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.p_full[t]);
+      l += masked ? exponentials<T, 0>(x, P.scale_log2, m, ts, c.p_full[t], lane)
+                  : exponentials<T, S::kFma>(x, P.scale_log2, m, ts, c.p_full[t], lane);
     }
     if (tiles[t] > 0 && fine) {
       fine = await(c, &c.pv_done[t], (tiles[t] - 1) & 1, a.status);
