@@ -19,7 +19,9 @@ namespace mk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens of a block
+constexpr int kMaxTokens = 4;   // tokens of a block
+constexpr int kFewTokens = 512; // up to here one
+constexpr int kBatch = 2;       // pieces a thread has in flight
 
 struct AppendParams {
   mk_append_args a;
@@ -30,7 +32,7 @@ template <class T, int D, int TOK>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int H = D / 2, PIECES = D / 16;  // pairs of a head; 16-byte pieces of half a head
   const mk_append_args& a = P.a;
-  __shared__ float2 turn[TOK][H];          // (cos, sin)
+  __shared__ __align__(16) float2 turn[TOK][H];  // (cos, sin)
   __shared__ long long dest[TOK];          // first element of the token's row in head 0 of its page, or -1
   __shared__ int where[TOK];               // position, or -1: row behind the last sequence
   const int t0 = blockIdx.x * TOK;
@@ -76,47 +78,67 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
   __syncthreads();
 
+  // pieces: 8 elements of a head's first half and the 8 that they turn with; kBatch of them are in flight a thread
   const int hq = a.q ? a.n_q_heads : 0, hkv = a.pages.n_kv_heads;
-  const int per_token = (hq + 2 * hkv) * PIECES;
-  for (int i = threadIdx.x; i < TOK * per_token; i += kThreads) {
-    const int tok = i / per_token, r = i % per_token, head = r / PIECES, c = (r % PIECES) * 8;
-    if (dest[tok] < 0) continue;
-    const long long t = t0 + tok;
-    const T* src;
-    T* dst;
-    if (head < hq) {
-      src = static_cast<const T*>(a.q) + t * a.q_row_stride + head * a.q_head_stride;
-      dst = static_cast<T*>(a.q_out) + t * a.qo_row_stride + head * a.qo_head_stride;
-    } else if (head < hq + hkv) {
-      const int h = head - hq;
-      src = static_cast<const T*>(a.k) + t * a.k_row_stride + h * a.k_head_stride;
-      dst = static_cast<T*>(a.pages.k) + dest[tok] + h * a.pages.head_stride;
-    } else {
-      const int h = head - hq - hkv;
-      src = static_cast<const T*>(a.v) + t * a.v_row_stride + h * a.v_head_stride;
-      dst = static_cast<T*>(a.pages.v) + dest[tok] + h * a.pages.head_stride;
-    }
-    uint4 lo = *reinterpret_cast<const uint4*>(src + c), hi = *reinterpret_cast<const uint4*>(src + c + H);
-    if (head < hq + hkv && a.rope_theta != 0.0) {
-      uint32_t* l = &lo.x;
-      uint32_t* h = &hi.x;
+  const int per_token = (hq + 2 * hkv) * PIECES, all = TOK * per_token;
+  for (int i0 = threadIdx.x; i0 < all; i0 += kThreads * kBatch) {
+    uint4 lo[kBatch], hi[kBatch];
+    T* dst[kBatch];
+    int turned[kBatch];  // token of the block * H + first pair, or -1: not turned
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = Elem<T>::unpack(l[j]), y = Elem<T>::unpack(h[j]);
-        const float2 u = turn[tok][c + 2 * j], w = turn[tok][c + 2 * j + 1];
-        l[j] = Elem<T>::pack(x.x * u.x - y.x * u.y, x.y * w.x - y.y * w.y);
-        h[j] = Elem<T>::pack(y.x * u.x + x.x * u.y, y.y * w.x + x.y * w.y);
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kThreads;
+      dst[u] = nullptr;
+      turned[u] = -1;
+      if (i >= all) continue;
+      const int tok = TOK == 1 ? 0 : i / per_token, r = i - tok * per_token, head = r / PIECES, c = (r % PIECES) * 8;
+      if (dest[tok] < 0) continue;
+      const long long t = t0 + tok;
+      const T* src;
+      if (head < hq) {
+        src = static_cast<const T*>(a.q) + t * a.q_row_stride + head * a.q_head_stride;
+        dst[u] = static_cast<T*>(a.q_out) + t * a.qo_row_stride + head * a.qo_head_stride;
+      } else if (head < hq + hkv) {
+        const int h = head - hq;
+        src = static_cast<const T*>(a.k) + t * a.k_row_stride + h * a.k_head_stride;
+        dst[u] = static_cast<T*>(a.pages.k) + dest[tok] + h * a.pages.head_stride;
+      } else {
+        const int h = head - hq - hkv;
+        src = static_cast<const T*>(a.v) + t * a.v_row_stride + h * a.v_head_stride;
+        dst[u] = static_cast<T*>(a.pages.v) + dest[tok] + h * a.pages.head_stride;
       }
+      if (head < hq + hkv && a.rope_theta != 0.0) turned[u] = tok * H + c;
+      lo[u] = *reinterpret_cast<const uint4*>(src + c);
+      hi[u] = *reinterpret_cast<const uint4*>(src + c + H);
+      dst[u] += c;
     }
-    *reinterpret_cast<uint4*>(dst + c) = lo;
-    *reinterpret_cast<uint4*>(dst + c + H) = hi;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (!dst[u]) continue;
+      if (turned[u] >= 0) {
+        const float4* cs = reinterpret_cast<const float4*>(&turn[0][0] + turned[u]);
+        uint32_t* l = &lo[u].x;
+        uint32_t* h = &hi[u].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = Elem<T>::unpack(l[j]), y = Elem<T>::unpack(h[j]);
+          const float4 w = cs[j];  // (cos, sin) of two pairs
+          l[j] = Elem<T>::pack(x.x * w.x - y.x * w.y, x.y * w.z - y.y * w.w);
+          h[j] = Elem<T>::pack(y.x * w.x + x.x * w.y, y.y * w.z + x.y * w.w);
+        }
+      }
+      *reinterpret_cast<uint4*>(dst[u]) = lo[u];
+      *reinterpret_cast<uint4*>(dst[u] + H) = hi[u];
+    }
   }
 }
 
 template <class T, int D>
 mk_status launch(const AppendParams& P, cudaStream_t s, std::string& err) {
+  // A block's tokens share its prologue (sequence search, angles); few tokens go one to a block, so that more SMs take part.
   const int n = P.a.n_tokens;
-  append_kernel<T, D, kMaxTokens><<<(n + kMaxTokens - 1) / kMaxTokens, kThreads, 0, s>>>(P);
+  if (n <= kFewTokens) append_kernel<T, D, 1><<<n, kThreads, 0, s>>>(P);
+  else append_kernel<T, D, kMaxTokens><<<(n + kMaxTokens - 1) / kMaxTokens, kThreads, 0, s>>>(P);
   return cuda_result(cudaGetLastError(), "mk_append_kv launch", err);
 }
 

@@ -35,19 +35,25 @@
 namespace mk {
 namespace {
 
-constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // (registers move between whole warpgroups)
 constexpr int kRows = 128;   // rows of a tile, keys of a tile
+constexpr int kTiles64 = 1;           // row tiles of a block at D = 64
 constexpr int kParts = 2;            // parts of a P tile, handed to the MMAs one by one
 constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
 constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait
 
-template <int D>
+// TILES: row tiles of a block
+template <int D, int TILES>
 struct Shape {
+  static constexpr int kSoftmaxWarps = 4 * TILES;
+  static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // (registers move between whole warpgroups)
+  static constexpr int kBlocksPerSm = TILES == 1 ? 2 : 1;
+  // registers of a thread: at launch 64K / (threads of an SM), then softmax and other warps
+  static constexpr int kMore = TILES == 1 ? 200 : 208, kLess = TILES == 1 ? 56 : 80;
+  static constexpr int kTmem = TILES == 1 ? 256 : 512;       // columns
   static constexpr int kTile = kRows * D * 2;        // bytes of 128 rows
-  static constexpr int kStages = D == 64 ? 8 : 4;    // ring of K and V tiles
+  static constexpr int kStages = D == 64 ? (TILES == 1 ? 5 : 8) : 4;  // ring of K and V tiles
   static constexpr int kFma = D == 64 ? 2 : 1;       // of 8 exponentials, how many go over the FMA pipes
-  static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024;
+  static constexpr int kSmem = (TILES + kStages) * kTile + 1024;
 };
 
 struct PromptParams {
@@ -55,7 +61,7 @@ struct PromptParams {
   mk_prompt_args a;
   float scale_log2;
   int group, tokens;   // G; tokens of a row tile
-  int pairs;           // upper bound on row-tile pairs of all sequences
+  int blocks;          // upper bound on blocks of row tiles of all sequences
   int span, per_span;  // keys of a page (or of all), key tiles that cover them
   int box;             // key rows of a TMA box
 };
@@ -64,7 +70,7 @@ struct Control {
   uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2][kParts], pv_done[2], v_tail;
   uint32_t tmem;
   int abort;
-  int warp_sum[kSoftmaxWarps];
+  int warp_sum[8];
   int found;
   int seq, pair;
 };
@@ -270,19 +276,20 @@ struct Seq {
   }
 };
 
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams P) {
-  using S = Shape<D>;
-  constexpr int HALVES = D / 64;
+template <class T, int D, int TILES>
+__global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kBlocksPerSm)
+    prompt_kernel(const __grid_constant__ PromptParams P) {
+  using S = Shape<D, TILES>;
+  constexpr int HALVES = D / 64, kSoftmaxWarps = S::kSoftmaxWarps, kO = 128 * TILES;
   extern __shared__ unsigned char raw[];
   __shared__ Control c;
   unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  unsigned char* sq = smem;                  // [2 tiles][HALVES][128][64]
-  unsigned char* ring = smem + 2 * S::kTile; // [kStages][HALVES][128][64]
+  unsigned char* sq = smem;                      // [TILES][HALVES][128][64]
+  unsigned char* ring = smem + TILES * S::kTile; // [kStages][HALVES][128][64]
   const mk_prompt_args& a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kvh = blockIdx.x % a.pages.n_kv_heads;
-  const int want = P.pairs - 1 - (int)(blockIdx.x / a.pages.n_kv_heads);  // long rows (the last) first
+  const int want = P.blocks - 1 - (int)(blockIdx.x / a.pages.n_kv_heads);  // long rows (the last) first
 
   // ---- which sequence and pair of row tiles: counted over the sequences, 256 at a time
   if (tid == 0) {
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const int b = b0 + tid;
       if (b < a.batch) {
         const int q0 = min(max(__ldg(a.cu_q + b), 0), a.n_tokens), q1 = min(__ldg(a.cu_q + b + 1), a.n_tokens);
-        mine = (max(q1 - q0, 0) + 2 * P.tokens - 1) / (2 * P.tokens);
+        mine = (max(q1 - q0, 0) + TILES * P.tokens - 1) / (TILES * P.tokens);
       }
       sum = mine;
 #pragma unroll
@@ -327,16 +334,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
   Seq s;
   s.load(P, c.seq);
-  const int first = c.pair * 2 * P.tokens;  // the block's first query
-  int tiles[2];                             // key tiles of each row tile
+  const int first = c.pair * TILES * P.tokens;  // the block's first query
+  int tiles[TILES], n_tiles = 0;            // key tiles of each row tile
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < TILES; ++t) {
     const int last = min(s.n, first + (t + 1) * P.tokens) - 1;
     const int seen = last >= first + t * P.tokens ? s.limit(P, last) : 0;
     const int full = seen > 0 ? (seen - 1) / P.span : 0;
     tiles[t] = seen > 0 ? full * P.per_span + (seen - full * P.span + kRows - 1) / kRows : 0;
+    n_tiles = max(n_tiles, tiles[t]);
   }
-  const int n_tiles = max(tiles[0], tiles[1]);
   // the key tile that the sequence ends inside, where this block reads it: the last one
   int ragged = -1;
   if (n_tiles > 0 && s.m - (((n_tiles - 1) / P.per_span) * P.span + ((n_tiles - 1) % P.per_span) * kRows) < kRows) ragged = n_tiles - 1;
@@ -348,28 +355,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&c.kv_full[i], 1);
       mbar_init(&c.kv_empty[i], 1);
     }
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < TILES; ++t) {
       mbar_init(&c.s_full[t], 1);
       for (int i = 0; i < kParts; ++i) mbar_init(&c.p_full[t][i], 4);
       mbar_init(&c.pv_done[t], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kSoftmaxWarps) tmem_alloc(&c.tmem, 512);
+  if (warp == kSoftmaxWarps) tmem_alloc(&c.tmem, S::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = c.tmem;  // S0, S1 at columns 0 and 128, O0, O1 at 256 and 256 + D
+  const uint32_t tmem = c.tmem;  // S of tile t at column 128 t, O at kO + D t
 
-  // registers: 2 x 128 x 208 + 128 x 80 of the 384 x 168 that the block was launched with
+  // (registers of a block, two tiles: 256 x 208 + 128 x 80 <= 384 x 168 at launch; one: 128 x (200 + 56) = 256 x 128)
   if (warp >= kSoftmaxWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kLess));
     if (warp == kSoftmaxWarps + 1) {
     // ---- loads
     if (n_tiles > 0) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(&c.q_full, 2u * HALVES * P.tokens * P.group * 128);
-        for (int t = 0; t < 2; ++t)
+        mbar_arrive_expect_tx(&c.q_full, (uint32_t)(TILES * HALVES * 128) * P.tokens * P.group);
+        for (int t = 0; t < TILES; ++t)
           for (int h = 0; h < HALVES; ++h)
             tma_load_3d(sq + t * S::kTile + h * (kRows * 128), &P.tq, 64 * h, kvh * P.group, s.q0 + first + t * P.tokens,
                         &c.q_full);
@@ -428,14 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < kRows / 16 / kParts; ++i) {
             const int k = part * (kRows / 16 / kParts) + i;
-            umma_ts(tmem + 256u + D * t, tmem + 128u * t + 8u * k, v_lo + stage * (S::kTile / 16) + 128u * k, id_pv, more || i);
+            umma_ts(tmem + kO + D * t, tmem + 128u * t + 8u * k, v_lo + stage * (S::kTile / 16) + 128u * k, id_pv, more || i);
           }
         };
         bool fine = await_lane(c, &c.q_full, 0, a.status) && await_lane(c, &c.kv_full[0], 0, a.status);
         if (fine) {
           tc_fence_after();
-          if (tiles[0] > 0) qk(0, 0);
-          if (tiles[1] > 0) qk(1, 0);
+#pragma unroll
+          for (int t = 0; t < TILES; ++t)
+            if (tiles[t] > 0) qk(t, 0);
           umma_commit(&c.kv_empty[0]);
         }
         for (int j = 0; j < n_tiles && fine; ++j) {
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (!fine) break;
           bool k_here = false;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < TILES; ++t) {
             if (j < tiles[t]) {
 #pragma unroll
               for (int i = 0; i < kParts; ++i) {
@@ -485,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
   } else {
     // ---- softmax: a thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMore));
     const int t = warp >> 2, r = tid & 127;
     const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + 128u * t;
-    const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + 256u + D * t;
+    const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kO + D * t;
     const int token = first + t * P.tokens + r / P.group;
     const bool row_live = r < P.tokens * P.group && token < s.n;
     const int limit = row_live ? s.limit(P, token) : 0;
@@ -576,17 +584,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncthreads();
   if (warp == kSoftmaxWarps) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, S::kTmem);
   }
 }
 
-template <class T, int D>
-mk_status launch(const PromptParams& P, cudaStream_t s, std::string& err) {
+template <class T, int D, int TILES>
+mk_status launch(PromptParams& P, cudaStream_t s, std::string& err) {
+  using S = Shape<D, TILES>;
+  const long long blocks = (long long)P.a.n_tokens / (TILES * P.tokens) + P.a.batch;
+  if (blocks * P.a.pages.n_kv_heads > 0x7fffffffll) {
+    err = "too many row tiles for one launch";
+    return MK_ERR_UNSUPPORTED;
+  }
+  P.blocks = (int)blocks;
   Device dev;
   cudaError_t e = current_device(dev);
-  if (e == cudaSuccess) e = allow<prompt_kernel<T, D>>(dev, Shape<D>::kSmem);
+  if (e == cudaSuccess) e = allow<prompt_kernel<T, D, TILES>>(dev, S::kSmem);
   if (e != cudaSuccess) return cuda_result(e, "mk_prompt_attention attributes", err);
-  prompt_kernel<T, D><<<P.pairs * P.a.pages.n_kv_heads, kThreads, Shape<D>::kSmem, s>>>(P);
+  prompt_kernel<T, D, TILES><<<P.blocks * P.a.pages.n_kv_heads, S::kThreads, S::kSmem, s>>>(P);
   return cuda_result(cudaGetLastError(), "mk_prompt_attention launch", err);
 }
 
@@ -600,12 +615,6 @@ mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err)
   P.scale_log2 = (a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
   P.group = a.n_q_heads / g.n_kv_heads;
   P.tokens = kRows / P.group;
-  const long long pairs = (long long)a.n_tokens / (2 * P.tokens) + a.batch;
-  if (pairs * g.n_kv_heads > 0x7fffffffll) {
-    err = "too many row tiles for one launch";
-    return MK_ERR_UNSUPPORTED;
-  }
-  P.pairs = (int)pairs;
   const bool paged = g.page_table != nullptr;
   P.box = paged && g.page_size < kRows ? g.page_size : kRows;
   P.span = paged ? std::max(g.page_size, kRows) : std::max(g.page_size, 1);
@@ -626,8 +635,8 @@ mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err)
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (g.dtype == MK_DTYPE_BF16)
-    return D == 64 ? launch<__nv_bfloat16, 64>(P, s, err) : launch<__nv_bfloat16, 128>(P, s, err);
-  return D == 64 ? launch<__half, 64>(P, s, err) : launch<__half, 128>(P, s, err);
+    return D == 64 ? launch<__nv_bfloat16, 64, kTiles64>(P, s, err) : launch<__nv_bfloat16, 128, 2>(P, s, err);
+  return D == 64 ? launch<__half, 64, kTiles64>(P, s, err) : launch<__half, 128, 2>(P, s, err);
 }
 
 }  // namespace mk

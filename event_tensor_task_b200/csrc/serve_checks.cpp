@@ -164,7 +164,7 @@ mk_status check_logits(const mk_logits_args& a, std::string& err) {
   if (a.history) {
     if (a.history_width < 0 || (a.rows > 1 && a.history_stride < a.history_width))
       return bad(err, "history_stride must be >= history_width >= 0");
-    if (a.history_width >= (1 << 30)) return bad(err, "history_width must be below 2^30");
+    if (a.history_width >= (1 << 28)) return bad(err, "history_width must be below 2^28");
   } else if (a.repetition || a.frequency || a.presence || a.history_lens || a.prompt_lens) {
     return bad(err, "penalties and history lengths need a history");
   }

@@ -104,7 +104,7 @@ def test_paged_refuses(path, value, status):
 @pytest.mark.parametrize("path,value,status", [
     ("rows", -1, INVALID), ("rows", 65536, INVALID), ("vocab", 0, INVALID), ("dtype", 3, INVALID), ("logits", 0, INVALID),
     ("logits", A + 2, INVALID), ("logits_stride", 99, INVALID), ("out_stride", 99, INVALID), ("out", A + 2, INVALID),
-    ("history_stride", 7, INVALID), ("history_width", -1, INVALID), ("history_width", 1 << 30, INVALID),
+    ("history_stride", 7, INVALID), ("history_width", -1, INVALID), ("history_width", 1 << 28, INVALID),
     ("history", 0, INVALID), ("bias_ids", 0, INVALID), ("bias_count", -1, INVALID), ("mask_stride", 3, INVALID),
     ("repetition", A + 1, INVALID)])
 def test_logits_refuses(path, value, status):
