@@ -369,99 +369,20 @@ class MoELayer:
 
 
 # ---------------------------------------------------------------- serving operators on tensors
-# (Single-token calls take a few microseconds on the device, so the checks here read each property of a tensor once
-# and leave what the C ABI checks to it.)
-def _refuse(what):
-    raise MkError(MK_ERR_INVALID_ARG, what)
+_tensors_module = None
 
 
-_DTYPES = {}
-
-
-def _dtypes():
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.bfloat16: MK_DTYPE_BF16, torch.float16: MK_DTYPE_FP16, torch.float32: MK_DTYPE_FP32})
-    return _DTYPES
-
-
-def _on(device, *tensors):
-    """Every given tensor is on ``device`` (a CUDA device)."""
-    if device.type != "cuda":
-        _refuse("the tensors must be on a CUDA device")
-    for t in tensors:
-        if t is not None and t.device != device:
-            _refuse(f"a tensor {list(t.shape)} is on {t.device}, the others on {device}")
-
-
-def _rows(name, t, shape, dtype):
-    """Address and strides (row, head) of a [rows][heads][head_dim] tensor whose last dimension is dense."""
-    if t.dtype != dtype or t.shape != shape:
-        _refuse(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    row, head, one = t.stride()
-    if one != 1 and shape[2] > 1:
-        _refuse(f"{name}: the last dimension must be dense")
-    # (the stride of a dimension of size 1 is not used)
-    return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
-
-
-def _array(name, t, dtype, n):
-    """Address of a dense array of n values (0: not given)."""
-    if t is None:
-        return 0
-    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
-        _refuse(f"{name} must be a dense {dtype} [{n}], not {t.dtype} {list(t.shape)}")
-    return t.data_ptr()
-
-
-def _pages(p, k, v, page_table, batch):
-    """Fill mk_kv_pages from k, v [n_pages][n_kv_heads][page_size][head_dim] and page_table int32 [batch][width]."""
-    import torch
-    shape, strides, dtype = k.shape, k.stride(), k.dtype
-    if len(shape) != 4 or v.shape != shape or v.dtype != dtype or dtype not in (torch.bfloat16, torch.float16):
-        _refuse("k and v pages must both be bf16 or fp16 [n_pages][n_kv_heads][page_size][head_dim]")
-    if 1 in shape or v.stride() != strides:  # (the stride of a dimension of size 1 is not used)
-        strides, other = ([0 if n == 1 else st for n, st in zip(shape, t.stride())] for t in (k, v))
-        if strides != other:
-            _refuse("k and v pages must have the same strides")
-    if strides[3] != 1:
-        _refuse("k and v pages must have a dense last dimension")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch:
-        _refuse("page_table must be int32 [batch][width]")
-    width = page_table.shape[1]
-    stride, one = page_table.stride()
-    if one != 1 and width > 1:
-        _refuse("page_table must have dense rows")
-    p.k, p.v, p.dtype = k.data_ptr(), v.data_ptr(), _dtypes()[dtype]
-    p.n_pages, p.n_kv_heads, p.page_size, p.head_dim = shape
-    p.page_stride, p.head_stride, p.row_stride = strides[0], strides[1], strides[2]
-    p.page_table, p.table_width, p.table_stride = page_table.data_ptr(), width, stride if batch > 1 else width
-
-
-class _launch_on:
-    """The stream a call goes to (``stream``, or the device's current one), made current with its device."""
-
-    def __init__(self, device, stream):
-        import torch
-        if stream is not None and stream.device != device:
-            _refuse(f"the stream is on {stream.device}, the tensors on {device}")
-        self.scope = None
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-            if torch.cuda.current_device() != device.index:
-                self.scope = torch.cuda.device(device)
-        else:
-            self.scope = torch.cuda.stream(stream)  # (outputs made here belong to it)
-        self.raw = stream.cuda_stream
-
-    def __enter__(self):
-        if self.scope is not None:
-            self.scope.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.scope is not None:
-            self.scope.__exit__(*exc)
+def _tensors():
+    """The module that marshals tensors for the functions below (csrc/tensors.cpp), bound to this library."""
+    global _tensors_module
+    if _tensors_module is None:
+        import torch  # noqa: F401 (the module links to torch's libraries)
+        module, library = _abi.load_tensors(), lib()
+        module.init(MkError, *(C.cast(getattr(library, name), C.c_void_p).value for name in (
+            "mk_append_kv", "mk_prompt_attention", "mk_paged_attention", "mk_paged_attention_workspace_bytes",
+            "mk_process_logits", "mk_last_error")))
+        _tensors_module = module
+    return _tensors_module
 
 
 def append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_theta=10000.0, q_out=None, status=None,
@@ -474,39 +395,10 @@ def append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_
     int32 [B][width]; one layer of a DenseDecoder's cache is such a pool, its slot ids [B][1] the table.
     ``rope_theta`` 0 (or None) stores the rows unturned.  Returns the turned queries: ``q_out`` (``q`` itself is
     allowed), or a new tensor, whose rows behind the last sequence are not written.  ``status``: int32 [1],
-    see include/mk.h."""
-    import torch
-    device = k.device
-    _on(device, q, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, q_out, status)
-    if k.dim() != 3:
-        _refuse("k must be [tokens][n_kv_heads][head_dim]")
-    batch, shape, dtype = ctx_lens.numel(), k.shape, k.dtype
-    a = mk_append_args()
-    p = a.pages
-    _pages(p, k_pages, v_pages, page_table, batch)
-    if k_pages.dtype != dtype or p.n_kv_heads != shape[1] or p.head_dim != shape[2]:
-        _refuse(f"k {dtype} {list(shape)} does not match the pages {k_pages.dtype} {list(k_pages.shape)}")
-    a.batch, a.n_tokens = batch, shape[0]
-    a.k, a.k_row_stride, a.k_head_stride = _rows("k", k, shape, dtype)
-    a.v, a.v_row_stride, a.v_head_stride = _rows("v", v, shape, dtype)
-    a.ctx_lens = _array("ctx_lens", ctx_lens, torch.int32, batch)
-    a.cu_seqlens = _array("cu_seqlens", cu_seqlens, torch.int32, batch + 1)
-    a.status = _array("status", status, torch.int32, 1)
-    a.rope_theta = rope_theta or 0.0
-    with _launch_on(device, stream) as s:
-        if q is not None:
-            if q.dim() != 3:
-                _refuse("q must be [tokens][n_q_heads][head_dim]")
-            qshape = torch.Size((shape[0], q.shape[1], shape[2]))
-            a.q, a.q_row_stride, a.q_head_stride = _rows("q", q, qshape, dtype)
-            if q_out is None:
-                q_out = q.new_empty(qshape)
-            a.q_out, a.qo_row_stride, a.qo_head_stride = _rows("q_out", q_out, qshape, dtype)
-            a.n_q_heads = qshape[1]
-        elif q_out is not None:
-            _refuse("q_out without q")
-        mk_append_kv(a, s)
-    return q_out
+    see include/mk.h.  Like all calls here it runs on ``stream`` (default: torch's current one), asynchronously, and
+    carries no gradient."""
+    return _tensors().append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_theta, q_out, status,
+                                stream)
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, page_table=None, kv_lens=None, causal=True, scale=None, out=None,
@@ -518,46 +410,7 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, page_table=None, kv_lens=None, ca
     ``kv_lens`` int32 [B] counts each sequence's keys, the new tokens' own among them.  Causal: the last query of a
     sequence sees all its keys, each one before it one less.  ``scale`` defaults to 1 / sqrt(D).  Returns ``out``, or
     a new tensor, whose rows behind the last sequence are not written."""
-    import torch
-    device = q.device
-    _on(device, k, v, cu_q, cu_k, page_table, kv_lens, out, status)
-    shape, dtype, batch = q.shape, q.dtype, cu_q.numel() - 1
-    if len(shape) != 3:
-        _refuse("q must be [tokens][n_q_heads][head_dim]")
-    a = mk_prompt_args()
-    p = a.pages
-    if page_table is not None:
-        if kv_lens is None or cu_k is not None:
-            _refuse("paged keys take kv_lens, not cu_k")
-        if page_table.numel() == 0 and batch > 0:
-            _refuse("page_table names no pages")
-        _pages(p, k, v, page_table, batch)
-        a.kv_lens = _array("kv_lens", kv_lens, torch.int32, batch)
-    else:
-        if kv_lens is not None:
-            _refuse("packed keys take cu_k, not kv_lens")
-        kshape = k.shape
-        if len(kshape) != 3 or k.dtype not in (torch.bfloat16, torch.float16):
-            _refuse("k and v must both be bf16 or fp16 [tokens][n_kv_heads][head_dim]")
-        p.k, p.row_stride, p.head_stride = _rows("k", k, kshape, k.dtype)
-        p.v, row, head = _rows("v", v, kshape, k.dtype)
-        if row != p.row_stride or head != p.head_stride:
-            _refuse("k and v must have the same strides")
-        p.dtype, p.n_pages = _dtypes()[k.dtype], 1
-        p.page_size, p.n_kv_heads, p.head_dim = kshape
-        a.cu_k = _array("cu_k", cu_q if cu_k is None else cu_k, torch.int32, batch + 1)
-    if k.dtype != dtype or p.head_dim != shape[2]:
-        _refuse(f"q {dtype} {list(shape)} does not match k {k.dtype} {list(k.shape)}")
-    a.batch, a.n_tokens, a.n_q_heads, a.causal, a.scale = batch, shape[0], shape[1], bool(causal), _scale(scale)
-    a.q, a.q_row_stride, a.q_head_stride = _rows("q", q, shape, dtype)
-    a.cu_q = _array("cu_q", cu_q, torch.int32, batch + 1)
-    a.status = _array("status", status, torch.int32, 1)
-    with _launch_on(device, stream) as s:
-        if out is None:
-            out = q.new_empty(shape)
-        a.out, a.o_row_stride, a.o_head_stride = _rows("out", out, shape, dtype)
-        mk_prompt_attention(a, s)
-    return out
+    return _tensors().prompt_attention(q, k, v, cu_q, cu_k, page_table, kv_lens, causal, scale, out, status, stream)
 
 
 def paged_attention(q, k_pages, v_pages, page_table, kv_lens, scale=None, out=None, workspace=None, status=None,
@@ -568,52 +421,7 @@ def paged_attention(q, k_pages, v_pages, page_table, kv_lens, scale=None, out=No
     the new token's own among them (0: a zero row).  ``workspace``: uint8, mk_paged_attention_workspace_bytes long and
     256-byte aligned (a torch allocation is), not to be shared by calls that overlap; by default one is allocated.
     Returns ``out`` [B][Hq][D], or a new tensor."""
-    import torch
-    device = q.device
-    _on(device, k_pages, v_pages, page_table, kv_lens, out, workspace, status)
-    shape, dtype = q.shape, q.dtype
-    if len(shape) != 3:
-        _refuse("q must be [batch][n_q_heads][head_dim]")
-    a = mk_paged_attn_args()
-    p = a.pages
-    _pages(p, k_pages, v_pages, page_table, shape[0])
-    if k_pages.dtype != dtype or p.head_dim != shape[2]:
-        _refuse(f"q {dtype} {list(shape)} does not match the pages {k_pages.dtype} {list(k_pages.shape)}")
-    a.batch, a.n_q_heads, a.scale = shape[0], shape[1], _scale(scale)
-    a.q, a.q_row_stride, a.q_head_stride = _rows("q", q, shape, dtype)
-    a.kv_lens = _array("kv_lens", kv_lens, torch.int32, shape[0])
-    a.status = _array("status", status, torch.int32, 1)
-    with _launch_on(device, stream) as s:
-        if out is None:
-            out = q.new_empty(shape)
-        a.out, a.o_row_stride, a.o_head_stride = _rows("out", out, shape, dtype)
-        if workspace is None:
-            workspace = torch.empty(mk_paged_attention_workspace_bytes(shape[0], shape[1], p.n_kv_heads, shape[2]),
-                                    dtype=torch.uint8, device=device)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            _refuse("workspace must be a dense uint8 tensor")
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-        mk_paged_attention(a, s)
-    return out
-
-
-def _scale(scale):
-    """The C ABI's scale: 0 stands for the default."""
-    if scale is None:
-        return 0.0
-    if not float(scale) > 0.0:
-        _refuse("scale must be above 0")
-    return float(scale)
-
-
-def _dense_rows(name, t, dtype, rows, width=None):
-    """Address and row stride of a [rows][width] tensor with dense rows."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or (width is not None and t.shape[1] != width):
-        _refuse(f"{name} must be {dtype} [{rows}][{'n' if width is None else width}], not {t.dtype} {list(t.shape)}")
-    row, one = t.stride()
-    if one != 1 and t.shape[1] > 1:
-        _refuse(f"{name} must have dense rows")
-    return t.data_ptr(), row if rows > 1 else t.shape[1]
+    return _tensors().paged_attention(q, k_pages, v_pages, page_table, kv_lens, scale, out, workspace, status, stream)
 
 
 def process_logits(logits, history=None, history_lens=None, prompt_lens=None, repetition=None, frequency=None,
@@ -625,46 +433,6 @@ def process_logits(logits, history=None, history_lens=None, prompt_lens=None, re
     (indptr int32 [rows + 1], ids int32 [n], values fp32 [n]); ``mask`` int32 [rows or 1][(vocab + 31) // 32] with a
     bit set for each allowed id.  Returns (out fp32 [rows][vocab], next_tokens int32 [rows]): the given tensors, or new
     ones; ``out`` may be ``logits`` itself.  A row in which nothing is left gets token -1."""
-    import torch
-    device, i32, f32 = logits.device, torch.int32, torch.float32
     indptr, ids, values = bias if bias is not None else (None, None, None)
-    _on(device, history, history_lens, prompt_lens, repetition, frequency, presence, indptr, ids, values, mask, out,
-        next_tokens, status)
-    dtype = _dtypes().get(logits.dtype)
-    if dtype is None or logits.dim() != 2:
-        _refuse("logits must be fp32, bf16 or fp16 [rows][vocab]")
-    R, V = logits.shape
-    a = mk_logits_args()
-    a.rows, a.vocab, a.dtype = R, V, dtype
-    a.logits, a.logits_stride = _dense_rows("logits", logits, logits.dtype, R, V)
-    if history is not None:
-        a.history, a.history_stride = _dense_rows("history", history, i32, R)
-        a.history_width = history.shape[1]
-        lens, prompts = _array("history_lens", history_lens, i32, R), _array("prompt_lens", prompt_lens, i32, R)
-        rep, freq = _array("repetition", repetition, f32, R), _array("frequency", frequency, f32, R)
-        pres = _array("presence", presence, f32, R)
-        if a.history:  # (a history without columns has no address)
-            a.history_lens, a.prompt_lens, a.repetition, a.frequency, a.presence = lens, prompts, rep, freq, pres
-    elif not (history_lens is prompt_lens is repetition is frequency is presence is None):
-        _refuse("penalties and history lengths need a history")
-    if bias is not None:
-        n = ids.numel()
-        addresses = _array("bias indptr", indptr, i32, R + 1), _array("bias ids", ids, i32, n), _array(
-            "bias values", values, f32, n)
-        if n:
-            a.bias_indptr, a.bias_ids, a.bias_values = addresses
-            a.bias_count = n
-    if mask is not None:
-        rows = mask.shape[0] if mask.dim() == 2 and mask.shape[0] == 1 else R
-        a.mask, stride = _dense_rows("mask", mask, i32, rows, (V + 31) // 32)
-        a.mask_stride = stride if rows > 1 else 0
-    a.status = _array("status", status, i32, 1)
-    with _launch_on(device, stream) as s:
-        if out is None:
-            out = torch.empty((R, V), dtype=f32, device=device)
-        if next_tokens is None:
-            next_tokens = torch.empty(R, dtype=i32, device=device)
-        a.out, a.out_stride = _dense_rows("out", out, f32, R, V)
-        a.next_tokens = _array("next_tokens", next_tokens, i32, R)
-        mk_process_logits(a, s)
-    return out, next_tokens
+    return _tensors().process_logits(logits, history, history_lens, prompt_lens, repetition, frequency, presence,
+                                     indptr, ids, values, mask, out, next_tokens, status, stream)

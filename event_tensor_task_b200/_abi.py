@@ -7,6 +7,7 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmk.so")
+TENSORS_PATH = os.path.join(HERE, "_tensors.so")
 
 MK_OK = 0
 MK_ERR_INVALID_ARG = -1
@@ -208,3 +209,15 @@ def load(path: str = LIB_PATH):
         fn.restype = res
         fn.argtypes = args
     return lib
+
+
+def load_tensors(path: str = TENSORS_PATH):
+    """The CPython module that marshals torch tensors into the structs above."""
+    import importlib.machinery
+    import importlib.util
+    if not os.path.exists(path):
+        raise RuntimeError(f"_tensors.so not found at {path}: build it with `python -m event_tensor_task_b200.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_tensors", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensors", loader))
+    loader.exec_module(module)
+    return module

@@ -1,4 +1,5 @@
-"""Build libmk.so in-tree with nvcc for sm_100a (B200).
+"""Build libmk.so in-tree with nvcc for sm_100a (B200), and _tensors.so, the
+module behind the serving operators' tensor calls, with the host compiler.
 
 ``python -m event_tensor_task_b200.build`` or ``build()`` from Python.  A
 source is compiled again when it, or any header under ``csrc/`` or
@@ -14,8 +15,10 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmk.so")
+TENSORS = os.path.join(HERE, "_tensors.so")
 OBJ = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CXX = os.environ.get("CXX", "g++")
 
 SOURCES = ["csrc/megakernel.cu", "csrc/plan.cpp", "csrc/api.cpp", "csrc/serve_checks.cpp", "csrc/append_kv.cu",
            "csrc/prompt_attn.cu", "csrc/paged_attn.cu", "csrc/logits.cu"]
@@ -31,7 +34,22 @@ def _newer(path, than) -> bool:
 
 def _stale() -> bool:
     deps = glob.glob(os.path.join(HERE, "csrc", "*")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    return any(_newer(d, LIB) for d in deps + [os.path.join(HERE, "build.py")])
+    deps.append(os.path.join(HERE, "build.py"))
+    return any(_newer(d, out) for out in (LIB, TENSORS) for d in deps)
+
+
+def _tensors_command():
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", TENSORS,
+            os.path.join(HERE, "csrc/tensors.cpp")] + ["-I" + i for i in include] + [
+                "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
 def _run(cmd, verbose):
@@ -39,7 +57,7 @@ def _run(cmd, verbose):
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, cwd=HERE, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+        raise RuntimeError(f"{cmd[0]} failed:\n" + r.stdout + r.stderr)
     if verbose and (r.stdout or r.stderr):
         print(r.stdout + r.stderr)
 
@@ -57,6 +75,8 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         objects.append(obj)
         if force or any(_newer(d, obj) for d in [src] + headers):
             todo.append([NVCC] + FLAGS + (extra or []) + ["-c", "-o", obj, src])
+    if force or any(_newer(d, TENSORS) for d in [os.path.join(HERE, "csrc/tensors.cpp")] + headers):
+        todo.append(_tensors_command())
     with ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as pool:
         list(pool.map(lambda cmd: _run(cmd, verbose), todo))
     _run([NVCC] + FLAGS + ["-shared", "-lcudart", "-o", LIB] + objects, verbose)

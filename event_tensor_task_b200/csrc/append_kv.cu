@@ -148,7 +148,11 @@ mk_status launch_append(const mk_append_args& a, void* stream, std::string& err)
   AppendParams P;
   P.a = a;
   const int D = a.pages.head_dim;
-  for (int p = 0; p < 64; ++p) P.freq[p] = a.rope_theta != 0.0 && p < D / 2 ? std::pow(a.rope_theta, -2.0 * p / D) : 0.0;
+  // theta^(-2p/D) = r^p, by squares of earlier ones (at most 12 roundings in double): 64 calls of pow would take
+  // longer than the kernel does for a few tokens
+  const double r = a.rope_theta != 0.0 ? std::pow(a.rope_theta, -2.0 / D) : 0.0;
+  P.freq[0] = 1.0;
+  for (int p = 1; p < 64; ++p) P.freq[p] = P.freq[p / 2] * P.freq[p / 2] * (p & 1 ? r : 1.0);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.pages.dtype == MK_DTYPE_BF16)
     return D == 64 ? launch<__nv_bfloat16, 64>(P, s, err) : launch<__nv_bfloat16, 128>(P, s, err);

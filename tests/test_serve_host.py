@@ -130,42 +130,79 @@ def test_null_arguments_and_empty_calls():
     assert lib.mk_process_logits(mk.mk_logits_args(vocab=9), 0) == mk.MK_OK
 
 
-def test_tensor_calls_refuse_what_the_struct_cannot_show():
-    """Types, shapes, strides and places, before any launch (CPU tensors: refused for that at the latest)."""
-    t = torch.zeros
-    q, kv = t((2, 4, 64), dtype=torch.bfloat16), t((3, 2, 16, 64), dtype=torch.bfloat16)
-    i = t((2, 3), dtype=torch.int32)
-    for call in (lambda: mk.paged_attention(q, kv, kv, i, i[:, 0]), lambda: mk.paged_attention(q[0], kv, kv, i, i[:, 0]),
-                 lambda: mk.prompt_attention(q, q, q, i[0]), lambda: mk.process_logits(t((2, 5))),
-                 lambda: mk.process_logits(t((2, 5), dtype=torch.float64)), lambda: mk.process_logits(t(5)),
-                 lambda: mk.append_kv(q, q, q, kv, kv, i, i[:, 0], i[0])):
-        with pytest.raises(mk.MkError) as e:
-            call()
-        assert e.value.status == INVALID
-    # the helpers behind them
-    def fill(*a):
-        p = mk.mk_kv_pages()
-        mk._pages(p, *a)
-        return p
+def tensors():
+    z = torch.zeros
+    return dict(q=z((4, 4, 64), dtype=torch.bfloat16), k=z((4, 2, 64), dtype=torch.bfloat16),
+                pool=z((3, 2, 16, 64), dtype=torch.bfloat16), table=z((2, 3), dtype=torch.int32),
+                lens=z(2, dtype=torch.int32), cu=z(3, dtype=torch.int32), logits=z((2, 70)),
+                hist=z((2, 5), dtype=torch.int32), row=z(2), mask=z((2, 3), dtype=torch.int32))
 
-    for bad in ((kv, kv.transpose(1, 2).contiguous().transpose(1, 2), i, 2),  # other strides
-                (kv, kv, i.long(), 2), (kv.float(), kv.float(), i, 2), (kv, kv, i, 3), (kv[0], kv[0], i, 2),
-                (kv, kv, i.T.contiguous().T, 2), (kv.transpose(2, 3), kv.transpose(2, 3), i, 2)):
-        with pytest.raises(mk.MkError):
-            fill(*bad)
-    with pytest.raises(mk.MkError):
-        mk._rows("q", q.transpose(1, 2), q.transpose(1, 2).shape, q.dtype)
-    with pytest.raises(mk.MkError):
-        mk._array("lens", i[:, 0], torch.int32, 2)  # not dense
-    with pytest.raises(mk.MkError):
-        mk._dense_rows("mask", i, torch.int32, 2, 4)
-    with pytest.raises(mk.MkError):
-        mk._scale(0.0)
-    p = fill(kv, kv, i, 2)
-    assert (p.n_pages, p.n_kv_heads, p.page_size, p.head_dim, p.table_width, p.table_stride) == (3, 2, 16, 64, 3, 3)
-    assert (p.page_stride, p.head_stride, p.row_stride) == (2048, 1024, 64)
-    p = fill(kv[:1], kv[1:2], i, 2)
-    assert (p.page_stride, p.head_stride, p.row_stride) == (0, 1024, 64)  # (one page: its stride is not used)
+
+def calls(x, **kw):
+    """The four calls on CPU tensors; `kw` replaces arguments."""
+    g = dict(x, **kw)
+    return dict(
+        append=lambda: mk.append_kv(g["q"], g["k"], g.get("v", x["k"]), g["pool"], g.get("vpool", g["pool"]), g["table"],
+                                    g["lens"], g["cu"], q_out=g.get("q_out")),
+        prompt=lambda: mk.prompt_attention(g["q"], g["k"], g.get("v", x["k"]), g["cu"], kv_lens=g.get("kv_lens"),
+                                           cu_k=g.get("cu_k"), scale=g.get("scale"), out=g.get("q_out")),
+        chunk=lambda: mk.prompt_attention(g["q"], g["pool"], g.get("vpool", g["pool"]), g["cu"], page_table=g["table"],
+                                          kv_lens=g["lens"], cu_k=g.get("cu_k")),
+        paged=lambda: mk.paged_attention(g["q"][:2], g["pool"], g.get("vpool", g["pool"]), g["table"], g["lens"],
+                                         scale=g.get("scale"), workspace=g.get("ws")),
+        logits=lambda: mk.process_logits(g["logits"], history=g["hist"], repetition=g["row"], mask=g["mask"],
+                                         bias=g.get("bias"), out=g.get("out"), next_tokens=g.get("next")))
+
+
+def test_tensor_calls_refuse_cpu_tensors():
+    """Everything in order but the place: refused for that, before any launch."""
+    for name, call in calls(tensors()).items():
+        with pytest.raises(mk.MkError, match="CUDA device") as e:
+            call()
+        assert e.value.status == INVALID, name
+
+
+@pytest.mark.parametrize("names,match,change", [
+    ("append", "k must be", lambda x: dict(k=x["k"][:, :1])),
+    ("append", "v must be", lambda x: dict(v=x["k"][:3])),
+    ("append", "v must be", lambda x: dict(v=x["k"].half())),
+    ("append prompt", "q must be", lambda x: dict(q=x["q"].float())),
+    ("append prompt paged", "q must be", lambda x: dict(q=x["q"][:, 0])),
+    ("append prompt paged", "q must be a tensor", lambda x: dict(q=[[1.0]] * 4)),
+    ("append prompt", "dense", lambda x: dict(q=x["q"].transpose(1, 2).contiguous().transpose(1, 2))),
+    ("append chunk paged", "page_table", lambda x: dict(table=x["table"].long())),
+    ("append chunk", "page_table", lambda x: dict(table=x["table"][:1])),
+    ("append chunk paged", "dense rows", lambda x: dict(table=x["table"].T.contiguous().T)),
+    ("append chunk paged", "same strides", lambda x: dict(vpool=x["pool"].transpose(1, 2).contiguous().transpose(1, 2))),
+    ("append chunk paged", "bf16 or fp16", lambda x: dict(pool=x["pool"].float())),
+    ("append chunk paged", "k and v pages", lambda x: dict(pool=x["pool"][0])),
+    ("append", "ctx_lens", lambda x: dict(lens=x["lens"].long())),
+    ("append", "cu_seqlens", lambda x: dict(cu=x["cu"][:2])),
+    ("chunk", "kv_lens must be", lambda x: dict(lens=torch.zeros((2, 2), dtype=torch.int32)[:, 0])),
+    ("prompt", "not kv_lens", lambda x: dict(kv_lens=x["lens"])),
+    ("prompt", "cu_k must be", lambda x: dict(cu_k=x["cu"][:2])),
+    ("prompt", "same strides", lambda x: dict(v=torch.zeros((4, 3, 64), dtype=torch.bfloat16)[:, :2])),
+    ("chunk", "not cu_k", lambda x: dict(cu_k=x["cu"])),
+    ("chunk", "names no pages", lambda x: dict(table=x["table"][:, :0])),
+    ("prompt paged", "scale", lambda x: dict(scale=0.0)),
+    ("prompt paged", "scale", lambda x: dict(scale=-1.0)),
+    ("paged", "workspace", lambda x: dict(ws=torch.zeros(9))),
+    ("logits", "logits must be", lambda x: dict(logits=x["logits"].double())),
+    ("logits", "logits must be", lambda x: dict(logits=x["logits"][0])),
+    ("logits", "dense rows", lambda x: dict(logits=x["logits"].T.contiguous().T)),
+    ("logits", "history must be", lambda x: dict(hist=x["hist"].long())),
+    ("logits", "need a history", lambda x: dict(hist=None)),
+    ("logits", "repetition", lambda x: dict(row=x["row"].double())),
+    ("logits", "mask must be", lambda x: dict(mask=x["mask"][:, :2])),
+    ("logits", "bias", lambda x: dict(bias=(x["cu"], x["lens"], None))),
+    ("logits", "bias values", lambda x: dict(bias=(x["cu"], x["lens"], torch.zeros(3)))),
+])
+def test_tensor_calls_refuse_types_shapes_and_strides(names, match, change):
+    x = tensors()
+    for name in names.split():
+        with pytest.raises(mk.MkError, match=match) as e:
+            calls(x, **change(x))[name]()
+        assert e.value.status == INVALID
 
 
 # ------------------------------------------------------------------------------------------------ the oracle's pins
