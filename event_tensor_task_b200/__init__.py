@@ -156,6 +156,11 @@ def mk_prompt_attention(args: mk_prompt_args, stream: int = 0):
     _check(lib().mk_prompt_attention(C.byref(args), stream))
 
 
+def mk_prompt_attention_workspace_bytes(batch: int, n_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                        max_keys: int) -> int:
+    return int(lib().mk_prompt_attention_workspace_bytes(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_keys))
+
+
 def mk_paged_attention_workspace_bytes(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return int(lib().mk_paged_attention_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim))
 
@@ -379,8 +384,8 @@ def _tensors():
         import torch  # noqa: F401 (the module links to torch's libraries)
         module, library = _abi.load_tensors(), lib()
         module.init(MkError, *(C.cast(getattr(library, name), C.c_void_p).value for name in (
-            "mk_append_kv", "mk_prompt_attention", "mk_paged_attention", "mk_paged_attention_workspace_bytes",
-            "mk_process_logits", "mk_last_error")))
+            "mk_append_kv", "mk_prompt_attention", "mk_prompt_attention_workspace_bytes", "mk_paged_attention",
+            "mk_paged_attention_workspace_bytes", "mk_process_logits", "mk_last_error")))
         _tensors_module = module
     return _tensors_module
 
@@ -402,15 +407,18 @@ def append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, page_table=None, kv_lens=None, causal=True, scale=None, out=None,
-                     status=None, stream=None):
+                     workspace=None, status=None, stream=None):
     """Attention over whole prompts, packed one after the other (mk_prompt_attention).
 
     q [T][Hq][D]; sequence b's queries are rows cu_q[b] .. cu_q[b + 1].  Without ``page_table``, k and v are
     [Tk][Hkv][D] with bounds ``cu_k`` (default ``cu_q``); with it they are cache pages as in :func:`append_kv` and
     ``kv_lens`` int32 [B] counts each sequence's keys, the new tokens' own among them.  Causal: the last query of a
     sequence sees all its keys, each one before it one less.  ``scale`` defaults to 1 / sqrt(D).  Returns ``out``, or
-    a new tensor, whose rows behind the last sequence are not written."""
-    return _tensors().prompt_attention(q, k, v, cu_q, cu_k, page_table, kv_lens, causal, scale, out, status, stream)
+    a new tensor, whose rows behind the last sequence are not written.  ``workspace``: uint8,
+    mk_prompt_attention_workspace_bytes long, not to be shared by calls that overlap; by default one is allocated where
+    the call can use it."""
+    return _tensors().prompt_attention(q, k, v, cu_q, cu_k, page_table, kv_lens, causal, scale, out, workspace, status,
+                                       stream)
 
 
 def paged_attention(q, k_pages, v_pages, page_table, kv_lens, scale=None, out=None, workspace=None, status=None,

@@ -121,7 +121,7 @@ class mk_prompt_args(C.Structure):
         ("causal", C.c_int), ("scale", C.c_float), ("q", C.c_void_p), ("out", C.c_void_p),
         ("q_row_stride", C.c_longlong), ("q_head_stride", C.c_longlong), ("o_row_stride", C.c_longlong),
         ("o_head_stride", C.c_longlong), ("cu_q", C.c_void_p), ("cu_k", C.c_void_p), ("kv_lens", C.c_void_p),
-        ("status", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t), ("status", C.c_void_p),
     ]
 
 
@@ -192,6 +192,7 @@ PROTOTYPES = {
     "mk_plan_destroy": (None, [C.c_void_p]),
     "mk_append_kv": (C.c_int, [C.POINTER(mk_append_args), C.c_void_p]),
     "mk_prompt_attention": (C.c_int, [C.POINTER(mk_prompt_args), C.c_void_p]),
+    "mk_prompt_attention_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_longlong]),
     "mk_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
     "mk_paged_attention": (C.c_int, [C.POINTER(mk_paged_attn_args), C.c_void_p]),
     "mk_process_logits": (C.c_int, [C.POINTER(mk_logits_args), C.c_void_p]),

@@ -307,6 +307,11 @@ mk_status mk_prompt_attention(const mk_prompt_args* a, void* stream) {
                                mk::check_prompt, mk::launch_prompt, stream);
 }
 
+size_t mk_prompt_attention_workspace_bytes(int batch, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                                           long long max_keys) {
+  return mk::prompt_workspace_bytes(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_keys);
+}
+
 size_t mk_paged_attention_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim) {
   return mk::paged_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim);
 }

@@ -38,6 +38,8 @@ namespace {
 constexpr int kRows = 128;   // rows of a tile, keys of a tile
 constexpr int kTiles64 = 1;           // row tiles of a block at D = 64
 constexpr int kParts = 2;            // parts of a P tile, handed to the MMAs one by one
+constexpr int kMostPieces = 64;       // of a block's keys
+constexpr int kLeastTiles = 6;        // key tiles of a piece: a block's way in and out costs about two
 constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
 constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait
 
@@ -50,9 +52,14 @@ struct Shape {
   // registers of a thread: at launch 64K / (threads of an SM), then softmax and other warps
   static constexpr int kMore = TILES == 1 ? 200 : 208, kLess = TILES == 1 ? 56 : 80;
   static constexpr int kTmem = TILES == 1 ? 256 : 512;       // columns
+  // At D = 64 TMEM holds P beside S, so S of the next key tile is computed while this one is in its softmax; at
+  // D = 128 S and O take all of it and P lies over S.
+  static constexpr bool kApart = D == 64;
+  static constexpr int kP = kApart ? TILES * (kRows + D) : 0, kPStep = kApart ? 64 : 128;  // P of tile t at column kP + kPStep t
   static constexpr int kTile = kRows * D * 2;        // bytes of 128 rows
   static constexpr int kStages = D == 64 ? (TILES == 1 ? 5 : 8) : 4;  // ring of K and V tiles
   static constexpr int kFma = D == 64 ? 2 : 1;       // of 8 exponentials, how many go over the FMA pipes
+  static constexpr int kPartial = TILES * kRows * (D + 2);   // floats of a piece's result: m, l, O of each row tile
   static constexpr int kSmem = (TILES + kStages) * kTile + 1024;
 };
 
@@ -61,18 +68,29 @@ struct PromptParams {
   mk_prompt_args a;
   float scale_log2;
   int group, tokens;   // G; tokens of a row tile
-  int blocks;          // upper bound on blocks of row tiles of all sequences
   int span, per_span;  // keys of a page (or of all), key tiles that cover them
   int box;             // key rows of a TMA box
+  int sms;             // SMs of the device
+  float* partial;      // results of pieces, or NULL: no sequence is cut into pieces
+  int slots;           // pieces that fit there
+};
+
+// One piece of work: a block's row tiles of one kv head against key tiles lo .. lo + max(count).
+struct Item {
+  int live;           // 0: no more work
+  int seq, kvh, first; // first: the block's first query within its sequence
+  int q0, n, k0, m;   // of the sequence (Seq)
+  int lo, count[2];   // first key tile; key tiles that each row tile sees from there
+  int slot;           // where the piece's result goes, or -1: to the output
 };
 
 struct Control {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2][kParts], pv_done[2], v_tail;
+  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], s_read[2], p_full[2][kParts], pv_done[2], v_tail;
+  uint64_t item_full[2], item_empty[2], next_block;
+  uint4 answer;       // of the request for the next block's number
+  Item item[2];
   uint32_t tmem;
   int abort;
-  int warp_sum[8];
-  int found;
-  int seq, pair;
 };
 
 // A whole warp waits for a phase; false (for all its lanes) after the limit or once another role has given up.
@@ -151,12 +169,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : MK_R8(r, 0), MK_R8(r, 8), MK_R8(r, 16), MK_R8(r, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      MK_W8(r, 0), MK_W8(r, 8), MK_W8(r, 16), MK_W8(r, 24)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : MK_R8(r, 0), MK_R8(r, 8)
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -276,6 +293,120 @@ struct Seq {
   }
 };
 
+// The order of an item's K and V tiles in the ring (n of each): as the MMAs
+// take them, K0 V0 K1 V1 .. where P lies over S, else K0 K1 V0 K2 V1 ..
+template <bool APART>
+__device__ __forceinline__ int ring_k(int j) { return APART ? max(0, 2 * j - 1) : 2 * j; }
+template <bool APART>
+__device__ __forceinline__ int ring_v(int j, int n) { return APART ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1; }
+
+// Which of an item's key tiles the sequence ends inside: its last one or none (-1).
+__device__ __forceinline__ int ragged_tile(const PromptParams& P, const Item& i, int n_tiles) {
+  const int j = i.lo + n_tiles - 1;
+  return n_tiles > 0 && i.m - ((j / P.per_span) * P.span + (j % P.per_span) * kRows) < kRows ? n_tiles - 1 : -1;
+}
+
+// How a sequence's work is laid out: row blocks, key tiles, pieces.
+template <int TILES>
+struct Work {
+  int blocks, tiles, pieces;  // tiles: of the last block, which sees the most keys
+  // key tiles that cover the first `seen` keys
+  static __device__ __forceinline__ int cover(const PromptParams& P, int seen) {
+    const int full = seen > 0 ? (seen - 1) / P.span : 0;
+    return seen > 0 ? full * P.per_span + (seen - full * P.span + kRows - 1) / kRows : 0;
+  }
+  __device__ __forceinline__ void load(const PromptParams& P, const Seq& s, int piece_tiles) {
+    blocks = (s.n + TILES * P.tokens - 1) / (TILES * P.tokens);
+    tiles = blocks > 0 ? cover(P, s.m) : 0;
+    pieces = P.partial && blocks > 0 && tiles > 0 ? min(kMostPieces, (tiles + piece_tiles - 1) / piece_tiles) : 1;
+  }
+  // the key tiles of all its blocks, as the mean of the first and the last
+  __device__ __forceinline__ long long total(const PromptParams& P, const Seq& s) const {
+    if (blocks == 0) return 0;
+    const int head = cover(P, s.limit(P, min(s.n, TILES * P.tokens) - 1));
+    return (long long)blocks * (head + tiles + 1) / 2 * P.a.pages.n_kv_heads;
+  }
+};
+
+// Key tiles of a piece: the whole call's work in equal shares of the SMs, not
+// below kLeastTiles.  A sequence whose blocks see more is cut into pieces of
+// that length; then no more than 4 sms of them carry results to be joined
+// (blocks * tiles <= 2 total, and pieces < 2 tiles / piece_tiles where there
+// are two or more).  Found by one warp, alike wherever it is asked for.
+template <int TILES>
+__device__ int piece_tiles_of(const PromptParams& P) {
+  if (!P.partial) return 0x7fffffff;
+  long long sum = 0;
+  for (int b = threadIdx.x & 31; b < P.a.batch; b += 32) {
+    Seq s;
+    s.load(P, b);
+    Work<TILES> w;
+    w.load(P, s, 1);
+    sum += w.total(P, s);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  return (int)max((long long)kLeastTiles, (sum + P.sms - 1) / P.sms);
+}
+
+// A warp walks the sequences, 32 at a time, for the one that item or joined
+// block number `want` falls into; numbers mostly ascend, and it goes on from
+// where it was.
+template <int TILES, bool JOIN>
+struct Walk {
+  int b0 = 0, piece_tiles;
+  long long base = 0, slot_base = 0;  // items, and results of pieces, of the sequences before b0
+  long long before, count, slots, slot_before;
+  Seq s;
+  Work<TILES> w;
+  __device__ __forceinline__ void fill(const PromptParams& P) {
+    const int lane = threadIdx.x & 31, b = b0 + lane;
+    count = slots = 0;
+    w.blocks = w.tiles = 0;
+    w.pieces = 1;
+    if (b < P.a.batch) {
+      s.load(P, b);
+      w.load(P, s, piece_tiles);
+      const long long rows = (long long)w.blocks * P.a.pages.n_kv_heads;
+      slots = w.pieces > 1 ? rows * w.pieces : 0;
+      count = JOIN ? (w.pieces > 1 ? rows : 0) : rows * w.pieces;
+    }
+    before = count;
+    slot_before = slots;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(~0u, before, d), p = __shfl_up_sync(~0u, slot_before, d);
+      if (lane >= d) {
+        before += o;
+        slot_before += p;
+      }
+    }
+    before -= count;
+    slot_before -= slots;
+  }
+  __device__ __forceinline__ void begin(const PromptParams& P) {
+    piece_tiles = piece_tiles_of<TILES>(P);
+    fill(P);
+  }
+  // the lane whose sequence holds `want`, or -1
+  __device__ __forceinline__ int find(const PromptParams& P, long long want) {
+    if (want < base) {
+      base = slot_base = 0;
+      b0 = 0;
+      fill(P);
+    }
+    for (;;) {
+      const unsigned hit = __ballot_sync(~0u, want >= base + before && want < base + before + count);
+      if (hit) return __ffs(hit) - 1;
+      if (b0 + 32 >= P.a.batch) return -1;
+      base += __shfl_sync(~0u, before + count, 31);
+      slot_base += __shfl_sync(~0u, slot_before + slots, 31);
+      b0 += 32;
+      fill(P);
+    }
+  }
+};
+
 template <class T, int D, int TILES>
 __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kBlocksPerSm)
     prompt_kernel(const __grid_constant__ PromptParams P) {
@@ -288,77 +419,27 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
   unsigned char* ring = smem + TILES * S::kTile; // [kStages][HALVES][128][64]
   const mk_prompt_args& a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kvh = blockIdx.x % a.pages.n_kv_heads;
-  const int want = P.blocks - 1 - (int)(blockIdx.x / a.pages.n_kv_heads);  // long rows (the last) first
 
-  // ---- which sequence and pair of row tiles: counted over the sequences, 256 at a time
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     c.abort = 0;
-    c.found = 0;
-  }
-  __syncthreads();
-  int base = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kSoftmaxWarps * 32) {
-    int mine = 0, sum = 0;
-    if (warp < kSoftmaxWarps) {
-      const int b = b0 + tid;
-      if (b < a.batch) {
-        const int q0 = min(max(__ldg(a.cu_q + b), 0), a.n_tokens), q1 = min(__ldg(a.cu_q + b + 1), a.n_tokens);
-        mine = (max(q1 - q0, 0) + TILES * P.tokens - 1) / (TILES * P.tokens);
-      }
-      sum = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(~0u, sum, d);
-        if (lane >= d) sum += o;
-      }
-      if (lane == 31) c.warp_sum[warp] = sum;
-    }
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < kSoftmaxWarps; ++w) {
-      if (w < warp) sum += c.warp_sum[w];
-      total += c.warp_sum[w];
-    }
-    if (warp < kSoftmaxWarps && want >= base + sum - mine && want < base + sum) {
-      c.seq = b0 + tid;
-      c.pair = want - (base + sum - mine);
-      c.found = 1;
-    }
-    __syncthreads();
-    base += total;
-    if (c.found) break;
-  }
-  if (!c.found) return;
-
-  Seq s;
-  s.load(P, c.seq);
-  const int first = c.pair * TILES * P.tokens;  // the block's first query
-  int tiles[TILES], n_tiles = 0;            // key tiles of each row tile
-#pragma unroll
-  for (int t = 0; t < TILES; ++t) {
-    const int last = min(s.n, first + (t + 1) * P.tokens) - 1;
-    const int seen = last >= first + t * P.tokens ? s.limit(P, last) : 0;
-    const int full = seen > 0 ? (seen - 1) / P.span : 0;
-    tiles[t] = seen > 0 ? full * P.per_span + (seen - full * P.span + kRows - 1) / kRows : 0;
-    n_tiles = max(n_tiles, tiles[t]);
-  }
-  // the key tile that the sequence ends inside, where this block reads it: the last one
-  int ragged = -1;
-  if (n_tiles > 0 && s.m - (((n_tiles - 1) / P.per_span) * P.span + ((n_tiles - 1) % P.per_span) * kRows) < kRows) ragged = n_tiles - 1;
-
-  if (tid == 0) {
     mbar_init(&c.q_full, 1);
+    mbar_init(&c.q_empty, 1);
     mbar_init(&c.v_tail, 1);
+    mbar_init(&c.next_block, 1);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&c.kv_full[i], 1);
       mbar_init(&c.kv_empty[i], 1);
     }
     for (int t = 0; t < TILES; ++t) {
       mbar_init(&c.s_full[t], 1);
+      mbar_init(&c.s_read[t], 4);
       for (int i = 0; i < kParts; ++i) mbar_init(&c.p_full[t][i], 4);
       mbar_init(&c.pv_done[t], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.item_full[i], 1);
+      mbar_init(&c.item_empty[i], kSoftmaxWarps + 3);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -368,59 +449,141 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
   tc_fence_after();
   const uint32_t tmem = c.tmem;  // S of tile t at column 128 t, O at kO + D t
 
+  // Every role runs the block's items one after the other, each at its own pace: the loads of the next item begin
+  // while this one is in its last softmax and on its way out.
   // (registers of a block, two tiles: 256 x 208 + 128 x 80 <= 384 x 168 at launch; one: 128 x (200 + 56) = 256 x 128)
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kLess));
-    if (warp == kSoftmaxWarps + 1) {
-    // ---- loads
-    if (n_tiles > 0) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&c.q_full, (uint32_t)(TILES * HALVES * 128) * P.tokens * P.group);
-        for (int t = 0; t < TILES; ++t)
-          for (int h = 0; h < HALVES; ++h)
-            tma_load_3d(sq + t * S::kTile + h * (kRows * 128), &P.tq, 64 * h, kvh * P.group, s.q0 + first + t * P.tokens,
-                        &c.q_full);
-      }
-      const int boxes = kRows / P.box;
-      const int pages = a.pages.page_table ? (s.m + a.pages.page_size - 1) / a.pages.page_size : 1;
-      int issued = 0;
+    if (warp == kSoftmaxWarps + 3) {
+      // ---- items: this block's number first, then those of blocks that have not begun, taken over one at a time
+      Walk<TILES, false> walk;
+      walk.begin(P);
+      const int kv_heads = a.pages.n_kv_heads;
+      long long number = blockIdx.x;
       bool fine = true;
-      for (int i = 0; i < 2 * n_tiles && fine; ++i) {
-        const int stage = i % S::kStages, j = i >> 1;
-        if (i >= S::kStages) fine = await(c, &c.kv_empty[stage], (i / S::kStages - 1) & 1, a.status);
-        if (!fine) break;
-        uint64_t* full = i == 2 * ragged + 1 ? &c.v_tail : &c.kv_full[stage];
-        if (lane == 0) mbar_arrive_expect_tx(full, S::kTile);
-        __syncwarp();
-        if (lane < boxes) {
-          int page = 0, row;
-          if (!a.pages.page_table) {
-            row = s.k0 + j * kRows;
-          } else {
-            const int key = (j / P.per_span) * P.span + (j % P.per_span) * kRows + lane * P.box;
-            const int at = key / a.pages.page_size;
-            row = key % a.pages.page_size;
-            page = at < pages ? page_of(a.pages, c.seq, at, a.status) : -1;
-            if (page < 0) page = a.pages.n_pages;  // out of range: the box reads as zeros
-          }
-          unsigned char* dst = ring + stage * S::kTile + lane * P.box * 128;
+      int k = 0;
+      for (uint32_t asked = 0; fine; ++asked) {
+        const int at = walk.find(P, number);
+        if (at >= 0) {
+          Item& it = c.item[k & 1];
+          if (lane == at) {
+            const Seq& s = walk.s;
+            const int pieces = walk.w.pieces, r = (int)(number - walk.base - walk.before);
+            const int block = walk.w.blocks - 1 - r / (kv_heads * pieces);  // a sequence's last rows see the most keys: first
+            const int kvh = r % kv_heads, piece = r / kv_heads % pieces;
+            it.first = block * TILES * P.tokens;
+            int tiles[2] = {0, 0};
 #pragma unroll
-          for (int h = 0; h < HALVES; ++h)
-            tma_load_4d(dst + h * (kRows * 128), (i & 1) ? &P.tv : &P.tk, 64 * h, row, kvh, page, full);
+            for (int t = 0; t < TILES; ++t) {
+              const int last = min(s.n, it.first + (t + 1) * P.tokens) - 1;
+              if (last >= it.first + t * P.tokens) tiles[t] = Work<TILES>::cover(P, s.limit(P, last));
+            }
+            const int n = max(tiles[0], tiles[1]), lo = (int)((long long)n * piece / pieces), hi = (int)((long long)n * (piece + 1) / pieces);
+            it.live = 1;
+            it.seq = walk.b0 + lane;
+            it.kvh = kvh;
+            it.q0 = s.q0;
+            it.n = s.n;
+            it.k0 = s.k0;
+            it.m = s.m;
+            it.lo = lo;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) it.count[t] = max(0, min(tiles[t], hi) - lo);
+            it.slot = -1;
+            if (pieces > 1) it.slot = (int)(walk.slot_base + walk.slot_before) + (block * kv_heads + kvh) * pieces + piece;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.item_full[k & 1]);
+          fine = await(c, &c.item_empty[k & 1], (k >> 1) & 1, a.status);  // all roles have it; the other slot is free
+          if (!fine) break;
+          ++k;
         }
+        uint32_t taken = 0, id = 0;
+        if (lane == 0) {
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(&c.next_block, 16);
+          asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                           smem_u32(&c.answer)),
+                       "r"(smem_u32(&c.next_block))
+                       : "memory");
+        }
+        fine = await(c, &c.next_block, asked & 1, a.status);
+        if (!fine) break;
+        asm volatile(
+            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+            : "=r"(taken), "=r"(id)
+            : "r"(smem_u32(&c.answer))
+            : "memory");
         __syncwarp();
-        issued = i + 1;
+        if (!taken) break;
+        number = id;
+      }
+      if (lane == 0) {
+        c.item[k & 1].live = 0;
+        mbar_arrive(&c.item_full[k & 1]);
+      }
+    } else if (warp == kSoftmaxWarps + 1) {
+      // ---- loads
+      int it = 0, loaded = 0;  // tiles of the ring so far; items with keys so far
+      bool fine = true;
+      for (int k = 0; fine; ++k) {
+        fine = await(c, &c.item_full[k & 1], (k >> 1) & 1, a.status);
+        if (!fine) break;
+        const Item item = c.item[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.item_empty[k & 1]);
+        if (!item.live) break;
+        const int n_tiles = max(item.count[0], item.count[1]);
+        if (n_tiles == 0) continue;
+        if (loaded > 0) fine = await(c, &c.q_empty, (loaded - 1) & 1, a.status);
+        if (!fine) break;
+        ++loaded;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&c.q_full, (uint32_t)(TILES * HALVES * 128) * P.tokens * P.group);
+          for (int t = 0; t < TILES; ++t)
+            for (int h = 0; h < HALVES; ++h)
+              tma_load_3d(sq + t * S::kTile + h * (kRows * 128), &P.tq, 64 * h, item.kvh * P.group,
+                          item.q0 + item.first + t * P.tokens, &c.q_full);
+        }
+        const int boxes = kRows / P.box, ragged = ragged_tile(P, item, n_tiles);
+        const int pages = a.pages.page_table ? (item.m + a.pages.page_size - 1) / a.pages.page_size : 1;
+        for (int i = 0; i < 2 * n_tiles; ++i, ++it) {
+          // (tile i of the ring order: is it V, and of which key tile)
+          const bool is_v = S::kApart ? i == 2 * n_tiles - 1 || (i > 0 && !(i & 1)) : i & 1;
+          const int stage = it % S::kStages, rel = S::kApart ? (is_v ? (i == 2 * n_tiles - 1 ? n_tiles - 1 : i / 2 - 1) : (i + 1) / 2) : i >> 1;
+          const int j = item.lo + rel;
+          if (it >= S::kStages) fine = await(c, &c.kv_empty[stage], (it / S::kStages - 1) & 1, a.status);
+          if (!fine) break;
+          uint64_t* full = is_v && rel == ragged ? &c.v_tail : &c.kv_full[stage];
+          if (lane == 0) mbar_arrive_expect_tx(full, S::kTile);
+          __syncwarp();
+          if (lane < boxes) {
+            int page = 0, row;
+            if (!a.pages.page_table) {
+              row = item.k0 + j * kRows;
+            } else {
+              const int key = (j / P.per_span) * P.span + (j % P.per_span) * kRows + lane * P.box;
+              const int at = key / a.pages.page_size;
+              row = key % a.pages.page_size;
+              page = at < pages ? page_of(a.pages, item.seq, at, a.status) : -1;
+              if (page < 0) page = a.pages.n_pages;  // out of range: the box reads as zeros
+            }
+            unsigned char* dst = ring + stage * S::kTile + lane * P.box * 128;
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+              tma_load_4d(dst + h * (kRows * 128), is_v ? &P.tv : &P.tk, 64 * h, row, item.kvh, page, full);
+          }
+          __syncwarp();
+        }
       }
       // no copy is in flight when the block leaves, even if another role has given up
-      drain(&c.q_full, 0);
-      for (int i = max(0, issued - S::kStages); i < issued; ++i) {
-        if (i == 2 * ragged + 1) drain(&c.v_tail, 0);
-        else drain(&c.kv_full[i % S::kStages], (i / S::kStages) & 1);
-      }
-    }
+      if (loaded > 0) drain(&c.q_full, (loaded - 1) & 1);
+      for (int i = max(0, it - S::kStages); i < it; ++i) drain(&c.kv_full[i % S::kStages], (i / S::kStages) & 1);
     } else if (warp == kSoftmaxWarps) {
       // ---- MMAs, by one thread (elect.sync: the compiler keeps the descriptors in uniform registers)
-      if (n_tiles > 0 && elect_one()) {
+      if (elect_one()) {
         constexpr uint32_t id_qk = idesc<T>(kRows, false), id_pv = idesc<T>(D, true);
         const uint32_t q_lo = desc_lo(sq, 1), k_lo = desc_lo(ring, 1), v_lo = desc_lo(ring, kRows * 128 / 16);
         auto qk = [&](int t, int stage) {
@@ -435,60 +598,116 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
 #pragma unroll
           for (int i = 0; i < kRows / 16 / kParts; ++i) {
             const int k = part * (kRows / 16 / kParts) + i;
-            umma_ts(tmem + kO + D * t, tmem + 128u * t + 8u * k, v_lo + stage * (S::kTile / 16) + 128u * k, id_pv, more || i);
+            umma_ts(tmem + kO + D * t, tmem + S::kP + S::kPStep * t + 8u * k, v_lo + stage * (S::kTile / 16) + 128u * k, id_pv, more || i);
           }
         };
-        bool fine = await_lane(c, &c.q_full, 0, a.status) && await_lane(c, &c.kv_full[0], 0, a.status);
-        if (fine) {
-          tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < TILES; ++t)
-            if (tiles[t] > 0) qk(t, 0);
-          umma_commit(&c.kv_empty[0]);
-        }
-        for (int j = 0; j < n_tiles && fine; ++j) {
-          const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % S::kStages, sk = ik % S::kStages;
-          fine = await_lane(c, &c.kv_full[sv], (iv / S::kStages) & 1, a.status);
+        int it = 0, loaded = 0, done[2] = {0, 0}, asked[2] = {0, 0};  // tiles of the ring, items with keys, P and S tiles of each row tile so far
+        bool fine = true;
+        for (int k = 0; fine; ++k) {
+          fine = await_lane(c, &c.item_full[k & 1], (k >> 1) & 1, a.status);
           if (!fine) break;
-          bool k_here = false;
+          const int live = c.item[k & 1].live;
+          int count[TILES], n_tiles = 0;
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
-            if (j < tiles[t]) {
+            count[t] = c.item[k & 1].count[t];
+            n_tiles = max(n_tiles, count[t]);
+          }
+          mbar_arrive(&c.item_empty[k & 1]);
+          if (!live) break;
+          if (n_tiles == 0) continue;
+          fine = await_lane(c, &c.q_full, loaded & 1, a.status);
+          ++loaded;
+          // S of key tile j of every row tile that sees it
+          auto scores = [&](int j) {
+            const int i = it + ring_k<S::kApart>(j);
+            fine = fine && await_lane(c, &c.kv_full[i % S::kStages], (i / S::kStages) & 1, a.status);
 #pragma unroll
-              for (int i = 0; i < kParts; ++i) {
-                fine = fine && await_lane(c, &c.p_full[t][i], j & 1, a.status);
-                if (!fine) break;
-                tc_fence_after();
-                pv(t, sv, i, j > 0 || i > 0);
-              }
-              if (!fine) break;
-              umma_commit(&c.pv_done[t]);
-            }
-            if (j + 1 < tiles[t]) {
-              if (!k_here) fine = await_lane(c, &c.kv_full[sk], (ik / S::kStages) & 1, a.status);
-              if (!fine) break;
+            for (int t = 0; t < TILES; ++t) {
+              if (j >= count[t] || !fine) continue;
+              // the S before has been read (where P lies over S: its P has been multiplied, which is issued before this)
+              if (S::kApart && asked[t] > 0) fine = await_lane(c, &c.s_read[t], (asked[t] - 1) & 1, a.status);
+              if (!fine) continue;
+              ++asked[t];
               tc_fence_after();
-              k_here = true;
-              qk(t, sk);
+              qk(t, i % S::kStages);
+            }
+            umma_commit(&c.kv_empty[i % S::kStages]);
+            if (j + 1 == n_tiles) umma_commit(&c.q_empty);
+          };
+          // O += P V of key tile j and row tile t
+          auto values = [&](int t, int j, int stage) {
+            // (the first P of an item is announced after O of the item before has been read)
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+              fine = fine && await_lane(c, &c.p_full[t][i], done[t] & 1, a.status);
+              if (!fine) return;
+              tc_fence_after();
+              pv(t, stage, i, j > 0 || i > 0);
+            }
+            umma_commit(&c.pv_done[t]);
+            ++done[t];
+          };
+          scores(0);
+          for (int j = 0; j < n_tiles && fine; ++j) {
+            const int iv = it + ring_v<S::kApart>(j, n_tiles), sv = iv % S::kStages;
+            if constexpr (S::kApart) {
+              if (j + 1 < n_tiles) scores(j + 1);
+              fine = fine && await_lane(c, &c.kv_full[sv], (iv / S::kStages) & 1, a.status);
+#pragma unroll
+              for (int t = 0; t < TILES; ++t)
+                if (j < count[t] && fine) values(t, j, sv);
+              umma_commit(&c.kv_empty[sv]);
+            } else {
+              const int ik = it + ring_k<false>(j + 1), sk = ik % S::kStages;
+              fine = await_lane(c, &c.kv_full[sv], (iv / S::kStages) & 1, a.status);
+              bool k_here = false;
+#pragma unroll
+              for (int t = 0; t < TILES; ++t) {
+                if (j < count[t] && fine) values(t, j, sv);
+                if (j + 1 < count[t] && fine) {
+                  if (!k_here) fine = await_lane(c, &c.kv_full[sk], (ik / S::kStages) & 1, a.status);
+                  if (!fine) break;
+                  tc_fence_after();
+                  k_here = true;
+                  ++asked[t];
+                  qk(t, sk);
+                }
+              }
+              umma_commit(&c.kv_empty[sv]);
+              if (j + 1 < n_tiles) umma_commit(&c.kv_empty[sk]);
+              if (j + 2 == n_tiles) umma_commit(&c.q_empty);
             }
           }
-          umma_commit(&c.kv_empty[sv]);
-          if (j + 1 < n_tiles) umma_commit(&c.kv_empty[sk]);
+          it += 2 * n_tiles;
         }
       }
       __syncwarp();
-    } else if (warp == kSoftmaxWarps + 2) {
+    } else {
       // ---- value rows behind the sequence's last key may hold anything, NaN too, and meet probabilities of zero:
       // cleared, before the tile counts as full
-      if (ragged >= 0 && await(c, &c.v_tail, 0, a.status)) {
-        const int live = s.m - ((ragged / P.per_span) * P.span + (ragged % P.per_span) * kRows);
-        unsigned char* v = ring + (2 * ragged + 1) % S::kStages * S::kTile + live * 128;
-        for (int i = lane; i < (kRows - live) * 8; i += 32)
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h) *reinterpret_cast<uint4*>(v + h * (kRows * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+      int it = 0, cleared = 0;
+      for (int k = 0;; ++k) {
+        if (!await(c, &c.item_full[k & 1], (k >> 1) & 1, a.status)) break;
+        const Item item = c.item[k & 1];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.kv_full[(2 * ragged + 1) % S::kStages]);
+        if (lane == 0) mbar_arrive(&c.item_empty[k & 1]);
+        if (!item.live) break;
+        const int n_tiles = max(item.count[0], item.count[1]), ragged = ragged_tile(P, item, n_tiles);
+        if (ragged >= 0) {
+          if (!await(c, &c.v_tail, cleared & 1, a.status)) break;
+          ++cleared;
+          const int j = item.lo + ragged, stage = (it + ring_v<S::kApart>(ragged, n_tiles)) % S::kStages;
+          const int live = item.m - ((j / P.per_span) * P.span + (j % P.per_span) * kRows);
+          unsigned char* v = ring + stage * S::kTile + live * 128;
+          for (int i = lane; i < (kRows - live) * 8; i += 32)
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) *reinterpret_cast<uint4*>(v + h * (kRows * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.kv_full[stage]);
+        }
+        it += 2 * n_tiles;
       }
     }
   } else {
@@ -497,87 +716,127 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
     const int t = warp >> 2, r = tid & 127;
     const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + 128u * t;
     const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kO + D * t;
-    const int token = first + t * P.tokens + r / P.group;
-    const bool row_live = r < P.tokens * P.group && token < s.n;
-    const int limit = row_live ? s.limit(P, token) : 0;
-    float m = 0.f, l = 0.f;
+    const uint32_t tp = tmem + ((uint32_t)(warp & 3) << 21) + S::kP + S::kPStep * t;
+    const int row_token = r / P.group, row_head = r % P.group;
+    int done = 0;  // S tiles so far
     bool fine = true;
-    for (int j = 0; j < tiles[t] && fine; ++j) {
-      fine = await(c, &c.s_full[t], j & 1, a.status);
+    for (int k = 0; fine; ++k) {
+      fine = await(c, &c.item_full[k & 1], (k >> 1) & 1, a.status);
       if (!fine) break;
-      tc_fence_after();
-      uint32_t x[kRows];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
-      tmem_wait_ld();
-      const int sub = (j % P.per_span) * kRows;
-      const int live = min(limit - ((j / P.per_span) * P.span + sub), P.span - sub);  // columns the row sees
-      const bool masked = __any_sync(~0u, live < kRows);
-      if (masked) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (i >= live) x[i] = 0xff800000u;
-      }
-      float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < kRows; i += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          part[e] = fmaxf(fmaxf(part[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + 4 + e]));
-      float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-      top *= P.scale_log2;
-      if (j == 0) {
-        m = top == -INFINITY ? 0.f : top;
-      } else if (__any_sync(~0u, top > m + kSlack)) {
-        fine = await(c, &c.pv_done[t], (j - 1) & 1, a.status);
+      const int live_item = c.item[k & 1].live, first = c.item[k & 1].first, kvh = c.item[k & 1].kvh, lo = c.item[k & 1].lo;
+      const int n_here = c.item[k & 1].count[t], slot = c.item[k & 1].slot;
+      Seq s;
+      s.q0 = c.item[k & 1].q0;
+      s.n = c.item[k & 1].n;
+      s.m = c.item[k & 1].m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.item_empty[k & 1]);
+      if (!live_item) break;
+      const int token = first + t * P.tokens + row_token;
+      const bool row_live = r < P.tokens * P.group && token < s.n;
+      const int limit = row_live ? s.limit(P, token) : 0;
+      float m = -INFINITY, l = 0.f;  // m: the reference, -inf until the row has seen a key
+      for (int j = 0; j < n_here && fine; ++j, ++done) {
+        fine = await(c, &c.s_full[t], done & 1, a.status);
         if (!fine) break;
         tc_fence_after();
-        const float up = top > m + kSlack ? top : m, f = ex2(m - up);
-        m = up;
-        l *= f;
+        uint32_t x[kRows];
 #pragma unroll
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
-          tmem_ld32(to + i, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st32(to + i, o);
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+        tmem_wait_ld();
+        if (S::kApart) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.s_read[t]);
         }
+        const int sub = ((lo + j) % P.per_span) * kRows;
+        const int live = min(limit - (((lo + j) / P.per_span) * P.span + sub), P.span - sub);  // columns the row sees
+        const bool masked = __any_sync(~0u, live < kRows);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (i >= live) x[i] = 0xff800000u;
+        }
+        float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kRows; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            part[e] = fmaxf(fmaxf(part[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + 4 + e]));
+        float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+        top *= P.scale_log2;
+        const bool moved = j > 0 && __any_sync(~0u, top > m + kSlack);
+        if (j > 0 && (S::kApart || moved)) {  // the product before is complete: O may be rescaled, P written
+          fine = await(c, &c.pv_done[t], (done - 1) & 1, a.status);
+          if (!fine) break;
+          tc_fence_after();
+        }
+        if (j == 0) {
+          m = top;
+        } else if (moved) {
+          const float up = top > m + kSlack ? top : m, f = up > m ? ex2(m - up) : 1.f;
+          m = up;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < D; i += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(to + i, o);
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        // (a masked score's probability is an exact zero only over the MUFU)
+        l += masked ? exponentials<T, 0>(x, P.scale_log2, ref, tp, c.p_full[t], lane)
+                    : exponentials<T, S::kFma>(x, P.scale_log2, ref, tp, c.p_full[t], lane);
       }
-      // (a masked score's probability is an exact zero only over the MUFU)
-      l += masked ? exponentials<T, 0>(x, P.scale_log2, m, ts, c.p_full[t], lane)
-                  : exponentials<T, S::kFma>(x, P.scale_log2, m, ts, c.p_full[t], lane);
-    }
-    if (tiles[t] > 0 && fine) {
-      fine = await(c, &c.pv_done[t], (tiles[t] - 1) & 1, a.status);
-      tc_fence_after();
-    }
-    if (fine) {
+      if (!fine) break;
+      if (n_here > 0) {
+        fine = await(c, &c.pv_done[t], (done - 1) & 1, a.status);
+        if (!fine) break;
+        tc_fence_after();
+      }
+      float* part = nullptr;
+      if (slot >= 0) {
+        part = P.partial + (long long)slot * S::kPartial + t * (kRows * (D + 2));
+        if (row_live && slot < P.slots) {
+          part[r] = m;
+          part[kRows + r] = l;
+        }
+        part += 2 * kRows + r * D;
+      }
       const float inv = limit > 0 ? 1.f / l : 0.f;
-      T* out = static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.o_row_stride +
-               (long long)(kvh * P.group + r % P.group) * a.o_head_stride;
+      T* out = static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.o_row_stride + (long long)(kvh * P.group + row_head) * a.o_head_stride;
 #pragma unroll
       for (int i = 0; i < D; i += 32) {
         uint32_t o[32];
-        if (tiles[t] > 0) {
+        if (n_here > 0) {
           tmem_ld32(to + i, o);
           tmem_wait_ld();
         }
-        if (row_live) {
+        if (!row_live) continue;
+        if (slot >= 0) {
+          if (n_here > 0 && slot < P.slots) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (limit > 0) {
-              w.x = Elem<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-              w.y = Elem<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-              w.z = Elem<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-              w.w = Elem<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-            }
-            *reinterpret_cast<uint4*>(out + i + e) = w;
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(part + i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
+          continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (limit > 0) {
+            w.x = Elem<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+            w.y = Elem<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            w.z = Elem<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+            w.w = Elem<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+          }
+          *reinterpret_cast<uint4*>(out + i + e) = w;
         }
       }
+      tc_fence_before();
     }
   }
   tc_fence_before();
@@ -588,28 +847,148 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
   }
 }
 
+// The pieces of one (row block, kv head) joined, a block for 32 rows of one of
+// its row tiles; launched while the first kernel runs.  The pieces' weights for
+// the rows are taken first, so that no output load waits for another.
+constexpr int kJoinRows = 32;
+
+template <class T, int D, int TILES>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PromptParams P) {
+  using S = Shape<D, TILES>;
+  constexpr int LANES = D / 4, PARTS = kRows / kJoinRows;  // a thread holds 4 values of a row
+  __shared__ int at[6];
+  __shared__ float weight[kMostPieces][kJoinRows];
+  const mk_prompt_args& a = P.a;
+  const int t = blockIdx.x / PARTS % TILES, first_row = blockIdx.x % PARTS * kJoinRows, tid = threadIdx.x;
+  if (tid < 32) {
+    Walk<TILES, true> walk;
+    walk.begin(P);
+    const long long number = blockIdx.x / (PARTS * TILES);
+    const int hit = walk.find(P, number);
+    if (tid == 0) at[0] = 0;
+    __syncwarp();
+    if (tid == hit) {
+      const int r = (int)(number - walk.base - walk.before), kv_heads = a.pages.n_kv_heads;
+      at[1] = (int)(walk.slot_base + walk.slot_before) + r * walk.w.pieces;  // (r = block * kv_heads + head)
+      at[2] = r / kv_heads * TILES * P.tokens + t * P.tokens;
+      at[3] = r % kv_heads;
+      at[4] = walk.s.q0;
+      at[5] = walk.s.n;
+      at[0] = walk.w.pieces;
+    }
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int pieces = at[0], slot = at[1];
+  if (pieces == 0 || slot + pieces > P.slots) return;
+  const int rows = min(kJoinRows, min(P.tokens, at[5] - at[2]) * P.group - first_row);  // (rows of tokens that exist)
+  if (rows <= 0) return;
+  const float* part = P.partial + (long long)slot * S::kPartial + t * (kRows * (D + 2));
+  // a row's weights are 2^(m_k - m) / sum_k l_k 2^(m_k - m); a piece in which the row sees no key (m_k = -inf) has
+  // weight 0 and is not read: its output may not be there
+  if (tid < rows) {
+    const float* p = part + first_row + tid;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) m = fmaxf(m, p[(long long)k * S::kPartial]);
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+      const float w = m == -INFINITY ? 0.f : ex2(p[(long long)k * S::kPartial] - m);
+      weight[k][tid] = w;
+      l += w * p[(long long)k * S::kPartial + kRows];
+    }
+    const float inv = m == -INFINITY ? 0.f : 1.f / l;
+    for (int k = 0; k < pieces; ++k) weight[k][tid] *= inv;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i0 = 0; i0 < kJoinRows * LANES; i0 += 256) {
+    const int i = i0 + tid, r = i / LANES, c = i % LANES * 4;
+    if (r >= rows) continue;
+    const float* p = part + 2 * kRows + (first_row + r) * D + c;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+      const float w = weight[k][r];
+      if (w == 0.f) continue;
+      const float4 v = *reinterpret_cast<const float4*>(p + (long long)k * S::kPartial);
+      o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+    }
+    const int row = first_row + r;
+    T* out = static_cast<T*>(a.out) + (long long)(at[4] + at[2] + row / P.group) * a.o_row_stride +
+             (long long)(at[3] * P.group + row % P.group) * a.o_head_stride + c;
+    *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
+  }
+}
+
+// Whether a call may cut sequences into pieces: its row blocks could leave SMs
+// idle, and there may be keys enough.
+bool may_cut(long long items, long long keys, int sms) { return items < 2ll * sms && keys >= 2ll * kLeastTiles * kRows; }
+
+template <int D, int TILES>
+long long items_of(const mk_prompt_args& a) {
+  const int tokens = kRows / (a.n_q_heads / a.pages.n_kv_heads);
+  return ((long long)a.n_tokens / (TILES * tokens) + a.batch) * a.pages.n_kv_heads;
+}
+
 template <class T, int D, int TILES>
 mk_status launch(PromptParams& P, cudaStream_t s, std::string& err) {
   using S = Shape<D, TILES>;
-  const long long blocks = (long long)P.a.n_tokens / (TILES * P.tokens) + P.a.batch;
-  if (blocks * P.a.pages.n_kv_heads > 0x7fffffffll) {
-    err = "too many row tiles for one launch";
-    return MK_ERR_UNSUPPORTED;
-  }
-  P.blocks = (int)blocks;
   Device dev;
   cudaError_t e = current_device(dev);
   if (e == cudaSuccess) e = allow<prompt_kernel<T, D, TILES>>(dev, S::kSmem);
   if (e != cudaSuccess) return cuda_result(e, "mk_prompt_attention attributes", err);
-  prompt_kernel<T, D, TILES><<<P.blocks * P.a.pages.n_kv_heads, S::kThreads, S::kSmem, s>>>(P);
-  return cuda_result(cudaGetLastError(), "mk_prompt_attention launch", err);
+  const mk_kv_pages& g = P.a.pages;
+  P.sms = dev.sms;
+  long long items = items_of<D, TILES>(P.a);
+  const long long keys = g.page_table ? (long long)g.table_width * g.page_size : g.page_size;
+  const long long slots = std::min<long long>(4 * dev.sms, P.a.workspace_bytes / (S::kPartial * sizeof(float)));
+  if (P.a.workspace && slots >= 4 * dev.sms && may_cut(items, keys, dev.sms)) {
+    P.partial = static_cast<float*>(P.a.workspace);
+    P.slots = (int)slots;
+    items += 2 * dev.sms;  // pieces: at most tiles / piece_tiles + 1 each, blocks * tiles <= 2 total
+  }
+  if (items > 0x7fffffffll) {
+    err = "too many row tiles for one launch";
+    return MK_ERR_UNSUPPORTED;
+  }
+  prompt_kernel<T, D, TILES><<<(unsigned)items, S::kThreads, S::kSmem, s>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !P.partial) return cuda_result(e, "mk_prompt_attention launch", err);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(slots / 2 * TILES * (kRows / kJoinRows)));  // (a joined block has two pieces or more)
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_result(cudaLaunchKernelEx(&cfg, join_kernel<T, D, TILES>, P), "mk_prompt_attention join launch", err);
 }
 
 }  // namespace
 
+size_t prompt_workspace_bytes(int batch, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, long long max_keys) {
+  Device dev;
+  if (batch < 1 || n_tokens < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads / n_kv_heads > kRows ||
+      current_device(dev) != cudaSuccess)
+    return 0;
+  mk_prompt_args a = {};
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.n_q_heads = n_q_heads;
+  a.pages.n_kv_heads = n_kv_heads;
+  const bool small = head_dim <= 64;
+  if (!may_cut(small ? items_of<64, kTiles64>(a) : items_of<128, 2>(a), max_keys, dev.sms)) return 0;
+  return (size_t)4 * dev.sms * (small ? Shape<64, kTiles64>::kPartial : Shape<128, 2>::kPartial) * sizeof(float);
+}
+
 mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err) {
   PromptParams P;
   P.a = a;
+  P.partial = nullptr;
+  P.slots = 0;
   const mk_kv_pages& g = a.pages;
   const int D = g.head_dim;
   P.scale_log2 = (a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;

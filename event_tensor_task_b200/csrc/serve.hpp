@@ -12,6 +12,7 @@ mk_status check_append(const mk_append_args& a, std::string& err);
 mk_status check_prompt(const mk_prompt_args& a, std::string& err);
 mk_status check_paged(const mk_paged_attn_args& a, std::string& err);
 mk_status check_logits(const mk_logits_args& a, std::string& err);
+size_t prompt_workspace_bytes(int batch, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, long long max_keys);
 size_t paged_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim);
 
 mk_status launch_append(const mk_append_args& a, void* stream, std::string& err);

@@ -110,6 +110,10 @@ mk_status check_prompt(const mk_prompt_args& a, std::string& err) {
     if (a.pages.n_pages != 1) return bad(err, "packed keys are one page: n_pages must be 1");
   }
   if (misaligned4(a.status)) return bad(err, "status must be 4-byte aligned");
+  if (a.workspace && (reinterpret_cast<uintptr_t>(a.workspace) & 255)) {
+    err = "workspace must be 256-byte aligned";
+    return MK_ERR_WORKSPACE;
+  }
   if (a.n_q_heads / a.pages.n_kv_heads > 128) {
     err = "more than 128 query heads per kv head";
     return MK_ERR_UNSUPPORTED;

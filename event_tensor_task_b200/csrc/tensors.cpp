@@ -29,6 +29,7 @@ struct Refusal {
 struct Abi {
   decltype(&mk_append_kv) append = nullptr;
   decltype(&mk_prompt_attention) prompt = nullptr;
+  decltype(&mk_prompt_attention_workspace_bytes) prompt_bytes = nullptr;
   decltype(&mk_paged_attention) paged = nullptr;
   decltype(&mk_paged_attention_workspace_bytes) paged_bytes = nullptr;
   decltype(&mk_process_logits) logits = nullptr;
@@ -234,11 +235,11 @@ PyObject* append(PyObject* const* o) {
   return result(o[9], out);
 }
 
-// q, k, v, cu_q, cu_k, page_table, kv_lens, causal, scale, out, status, stream
+// q, k, v, cu_q, cu_k, page_table, kv_lens, causal, scale, out, workspace, status, stream
 PyObject* prompt(PyObject* const* o) {
   const at::Tensor &q = needed(o[0], "q"), &k = needed(o[1], "k"), &v = needed(o[2], "v"), &cu_q = needed(o[3], "cu_q"),
                    *cu_k = given(o[4], "cu_k"), *table = given(o[5], "page_table"), *lens = given(o[6], "kv_lens"),
-                   *given_out = given(o[9], "out"), *status = given(o[10], "status");
+                   *given_out = given(o[9], "out"), *given_ws = given(o[10], "workspace"), *status = given(o[11], "status");
   mk_prompt_args a = {};
   mk_kv_pages& p = a.pages;
   if (cu_q.numel() < 1) refuse("cu_q must be int32 [batch + 1]");
@@ -272,10 +273,23 @@ PyObject* prompt(PyObject* const* o) {
   rows("q", q, n, heads, p.head_dim, k.scalar_type(), a.q, a.q_row_stride, a.q_head_stride);
   a.cu_q = static_cast<const int*>(array("cu_q", &cu_q, at::kInt, batch + 1));
   a.status = static_cast<int*>(array("status", status, at::kInt, 1));
-  Place place(q, {&k, &v, &cu_q, cu_k, table, lens, given_out, status}, o[11]);
+  if (given_ws && (given_ws->scalar_type() != at::kByte || !given_ws->is_contiguous())) refuse("workspace must be a dense uint8 tensor");
+  Place place(q, {&k, &v, &cu_q, cu_k, table, lens, given_out, given_ws, status}, o[12]);
   const at::Tensor out = given_out ? *given_out : at::empty(q.sizes(), q.options());
   rows("out", out, n, heads, p.head_dim, q.scalar_type(), a.out, a.o_row_stride, a.o_head_stride);
   apart("out", a.o_row_stride, a.o_head_stride, n, heads, p.head_dim);
+  at::Tensor ws;
+  if (given_ws) {
+    ws = *given_ws;
+  } else {
+    const size_t bytes = abi.prompt_bytes(a.batch, a.n_tokens, a.n_q_heads, p.n_kv_heads, p.head_dim,
+                                          (long long)p.page_size * (table ? p.table_width : 1));
+    if (bytes) ws = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
+  }
+  if (ws.defined()) {
+    a.workspace = ws.data_ptr();
+    a.workspace_bytes = static_cast<size_t>(ws.numel());
+  }
   done(abi.prompt(&a, place.raw));
   return result(o[9], out);
 }
@@ -399,24 +413,26 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (MkError, addresses of mk_append_kv, mk_prompt_attention, mk_paged_attention,
+// (MkError, addresses of mk_append_kv, mk_prompt_attention,
+// mk_prompt_attention_workspace_bytes, mk_paged_attention,
 // mk_paged_attention_workspace_bytes, mk_process_logits, mk_last_error)
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  void* f[6];
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "init takes the error class and six addresses");
+  void* f[7];
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "init takes the error class and seven addresses");
     return nullptr;
   }
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < 7; ++i) {
     f[i] = PyLong_AsVoidPtr(args[i + 1]);
     if (PyErr_Occurred()) return nullptr;
   }
   abi.append = reinterpret_cast<decltype(abi.append)>(f[0]);
   abi.prompt = reinterpret_cast<decltype(abi.prompt)>(f[1]);
-  abi.paged = reinterpret_cast<decltype(abi.paged)>(f[2]);
-  abi.paged_bytes = reinterpret_cast<decltype(abi.paged_bytes)>(f[3]);
-  abi.logits = reinterpret_cast<decltype(abi.logits)>(f[4]);
-  abi.last_error = reinterpret_cast<decltype(abi.last_error)>(f[5]);
+  abi.prompt_bytes = reinterpret_cast<decltype(abi.prompt_bytes)>(f[2]);
+  abi.paged = reinterpret_cast<decltype(abi.paged)>(f[3]);
+  abi.paged_bytes = reinterpret_cast<decltype(abi.paged_bytes)>(f[4]);
+  abi.logits = reinterpret_cast<decltype(abi.logits)>(f[5]);
+  abi.last_error = reinterpret_cast<decltype(abi.last_error)>(f[6]);
   Py_XDECREF(abi.error);
   abi.error = Py_NewRef(args[0]);
   Py_RETURN_NONE;
@@ -426,7 +442,7 @@ PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"init", MK_METHOD(init), METH_FASTCALL, nullptr},
     {"append_kv", MK_METHOD((call<append, 12>)), METH_FASTCALL, nullptr},
-    {"prompt_attention", MK_METHOD((call<prompt, 12>)), METH_FASTCALL, nullptr},
+    {"prompt_attention", MK_METHOD((call<prompt, 13>)), METH_FASTCALL, nullptr},
     {"paged_attention", MK_METHOD((call<paged, 10>)), METH_FASTCALL, nullptr},
     {"process_logits", MK_METHOD((call<logits, 15>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
