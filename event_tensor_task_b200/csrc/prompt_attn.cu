@@ -3,30 +3,42 @@
 //
 // Mathematics: out_i = sum_j p_ij v_j / sum_j p_ij, p_ij = 2^(c (q_i.k_j) - m_i),
 // c = scale log2 e, in one pass over the keys with a running reference m_i.
-// m_i follows the running maximum only when that has grown by more than 2^8:
-// the probabilities then stay below 2^8, exact in the same way, and the
-// accumulated output is rescaled a few times a row instead of at every tile.
+// m_i follows the running maximum only when that has grown by more than 8 in
+// the exponent: the probabilities then stay below 2^8, exact in the same way,
+// and the accumulated output is rescaled a few times a row instead of at every
+// tile.  P is rounded to the type for its product, as the tensor cores take it;
+// its sum is that of the unrounded values in fp32.
 //
 // Rows: the G = n_q_heads / n_kv_heads query heads that share a kv head are
 // stacked, so a tile of 128 rows is floor(128 / G) tokens times G heads (one
 // TMA box [tokens][G][64]); a short prompt fills a tile G times better and the
 // causal diagonal is G times narrower than with one head per tile.
 //
-// A block holds two such tiles (256 rows) and streams the keys past both:
-//   warps 0-3 / 4-7: softmax of tile 0 / 1, a thread per row: S from TMEM to
-//                    registers, maximum, exponentials, P (16 bit) back to TMEM
-//                    over S, at the end O / l to global memory;
-//   warp 8:          one thread issues the MMAs, S = Q K^T (Q, K from shared
+// A block holds one such tile (D = 64, two blocks an SM) or two (D = 128, one
+// block) and streams the keys past them:
+//   4 warps a tile:  softmax, a thread per row: S from TMEM to registers,
+//                    maximum, exponentials, P (16 bit) back to TMEM, at the end
+//                    O / l to global memory;
+//   a warp:          one thread issues the MMAs, S = Q K^T (Q, K from shared
 //                    memory, both K-major) and O += P V (P from TMEM, V from
 //                    shared memory, its N = dimensions contiguous);
-//   warp 9:          TMA loads, K and V tiles of 128 keys in a ring
-//                    (warps 10 and 11 fill up the warpgroup whose registers
-//                    the softmax warps take over).
-// While one tile is in its softmax, the other has the tensor pipe.
+//   a warp:          TMA loads, K and V tiles of 128 keys in a ring;
+//   a warp:          clears the rows of V behind a sequence's last key;
+//   a warp:          fetches the block's next piece of work (cluster launch
+//                    control: numbers of blocks that have not begun).
+// While one tile is in its softmax, the other has the tensor pipe.  Where few
+// rows meet many keys, the keys are cut into pieces that a second kernel joins.
 //
-// Bound: at D = 128 the two products and the exponentials take the same time
-// (128 x 128 scores: 1,024 cycles of the tensor pipe, 1,024 of the MUFU); at
-// D = 64 the exponentials take twice the products' time.
+// Bound: per tile of 128 x 128 scores the exponentials take 1,024 cycles of the
+// MUFU, the products 1,024 of the tensor pipe at D = 128 and 512 at D = 64.
+// Measured: a tile takes about 1,600 cycles at D = 128 (1,280 TFLOP/s at full
+// clock, 16k tokens, 32 heads; the power limit takes it to 1,130 when repeated)
+// and 1,350 at D = 64: a row's chain (S ready, maximum, exponentials, P, the
+// product's wait) and its ~600 instructions on two softmax warps a scheduler.
+// Tried and slower: two threads a row (2.13 against 1.80 ms on 16k tokens), an
+// eighth to a half of the exponentials as a polynomial on the FMA pipes (equal
+// at an eighth, 10 % slower at 3/8), two tiles a block at D = 64 (222 against
+// 204 us on eight packed prompts).
 #include <algorithm>
 #include <cmath>
 
@@ -37,7 +49,8 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a tile, keys of a tile
 constexpr int kTiles64 = 1;           // row tiles of a block at D = 64
-constexpr int kParts = 2;            // parts of a P tile, handed to the MMAs one by one
+constexpr int kParts = 2;            // halves of a P tile, handed to the MMAs one by one
+constexpr int kShares = 2, kSlots = 4 * kShares;  // (see piece_tiles_of)
 constexpr int kMostPieces = 64;       // of a block's keys
 constexpr int kLeastTiles = 6;        // key tiles of a piece: a block's way in and out costs about two
 constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
@@ -58,7 +71,6 @@ struct Shape {
   static constexpr int kP = kApart ? TILES * (kRows + D) : 0, kPStep = kApart ? 64 : 128;  // P of tile t at column kP + kPStep t
   static constexpr int kTile = kRows * D * 2;        // bytes of 128 rows
   static constexpr int kStages = D == 64 ? (TILES == 1 ? 5 : 8) : 4;  // ring of K and V tiles
-  static constexpr int kFma = D == 64 ? 2 : 1;       // of 8 exponentials, how many go over the FMA pipes
   static constexpr int kPartial = TILES * kRows * (D + 2);   // floats of a piece's result: m, l, O of each row tile
   static constexpr int kSmem = (TILES + kStages) * kTile + 1024;
 };
@@ -210,58 +222,41 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x of a pair on the FMA pipes, for x in [-125, 64] (smaller x as -125):
-// x = n + f with n whole and |f| <= 1/2 (Cody-Waite reduction by adding
-// 1.5 2^23), 2^f by a degree-4 polynomial, n into the exponent.  The
-// coefficients are those of the least relative error on [-1/2, 1/2] (Remez
-// exchange): 2^-18.5, far below a 16-bit probability's half step.
-__device__ __forceinline__ float2 ex2_fma(uint64_t x) {
-  float2 v = both(x);
-  x = pair(fmaxf(v.x, -125.f), fmaxf(v.y, -125.f));
-  const uint64_t magic = pair(12582912.f, 12582912.f);
-  const uint64_t t = add2(x, magic);
-  const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
-  uint64_t p = fma2(pair(0.009570102f, 0.009570102f), f, pair(0.055917859f, 0.055917859f));
-  p = fma2(p, f, pair(0.24024744f, 0.24024744f));
-  p = fma2(p, f, pair(0.69312179f, 0.69312179f));
-  p = fma2(p, f, pair(0.99999928f, 0.99999928f));
-  const float2 n = both(t), y = both(p);
-  return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(n.x) << 23)),
-                     __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(n.y) << 23)));
-}
-// p = 2^(c s - m) of the 128 scores in x, 16-bit pairs to TMEM at `dst`, each
-// part announced on `ready` when it is there; returns their sum.  FMA of 8 pairs go over the FMA pipes, the others over
-// the MUFU.
-template <class T, int FMA>
-__device__ __forceinline__ float exponentials(const uint32_t* x, float c, float m, uint32_t dst, uint64_t* ready, int lane) {
+// p = 2^(c s - m) of 64 scores, as 16-bit pairs to TMEM at `dst`, added to
+// `sum` two by two.  MAX: the maximum of these 64 and of 64 more in `others`
+// is taken on the way, in the issue slots that the MUFU leaves free.
+template <class T, bool MAX>
+__device__ __forceinline__ void exponentials(const uint32_t* x, const uint32_t* others, float c, float m, uint32_t dst,
+                                             uint64_t& sum, float& top) {
   const uint64_t cc = pair(c, c), mm = pair(-m, -m);
-  uint64_t sum[2] = {0, 0};
+  uint64_t part[2] = {0, 0};
+  float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < kRows; i += 32) {
+  for (int i = 0; i < 64; i += 32) {
     uint32_t p[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const uint64_t u = fma2(pair(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])), cc, mm);
-      float2 y;
-      if ((e * FMA) / 8 != ((e + 1) * FMA) / 8) {
-        y = ex2_fma(u);
-      } else {
-        y = both(u);
-        y = make_float2(ex2(y.x), ex2(y.y));
-      }
-      sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
+      const int at = i + 2 * e;
+      const float2 u = both(fma2(pair(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, mm));
+      const float2 y = make_float2(ex2(u.x), ex2(u.y));
+      part[e & 1] = add2(part[e & 1], pair(y.x, y.y));
       p[e] = Elem<T>::pack(y.x, y.y);
+      if (MAX) {
+        best[e & 1] = fmaxf(fmaxf(best[e & 1], __uint_as_float(x[at])), __uint_as_float(x[at + 1]));
+        best[2 + (e & 1)] = fmaxf(fmaxf(best[2 + (e & 1)], __uint_as_float(others[at])), __uint_as_float(others[at + 1]));
+      }
     }
     tmem_st16(dst + i / 2, p);
-    if ((i + 32) % (kRows / kParts) == 0) {
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ready + i / (kRows / kParts));
-    }
   }
-  const float2 a = both(add2(sum[0], sum[1]));
-  return a.x + a.y;
+  sum = add2(part[0], part[1]);
+  if (MAX) top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
+}
+// a part of P is in TMEM: announced
+__device__ __forceinline__ void announce(uint64_t* ready, int lane) {
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(ready);
 }
 
 // One sequence: its query rows, key rows and where they lie.
@@ -328,11 +323,11 @@ struct Work {
   }
 };
 
-// Key tiles of a piece: the whole call's work in equal shares of the SMs, not
+// Key tiles of a piece: the whole call's work in kShares shares for each SM, not
 // below kLeastTiles.  A sequence whose blocks see more is cut into pieces of
-// that length; then no more than 4 sms of them carry results to be joined
-// (blocks * tiles <= 2 total, and pieces < 2 tiles / piece_tiles where there
-// are two or more).  Found by one warp, alike wherever it is asked for.
+// that length; then no more than 4 kShares sms of them carry results to be
+// joined (blocks * tiles <= 2 total, and pieces < 2 tiles / piece_tiles where
+// there are two or more).  Found by one warp, alike wherever it is asked for.
 template <int TILES>
 __device__ int piece_tiles_of(const PromptParams& P) {
   if (!P.partial) return 0x7fffffff;
@@ -346,7 +341,7 @@ __device__ int piece_tiles_of(const PromptParams& P) {
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  return (int)max((long long)kLeastTiles, (sum + P.sms - 1) / P.sms);
+  return (int)max((long long)kLeastTiles, (sum + kShares * P.sms - 1) / (kShares * P.sms));
 }
 
 // A warp walks the sequences, 32 at a time, for the one that item or joined
@@ -751,46 +746,53 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
         }
         const int sub = ((lo + j) % P.per_span) * kRows;
         const int live = min(limit - (((lo + j) / P.per_span) * P.span + sub), P.span - sub);  // columns the row sees
-        const bool masked = __any_sync(~0u, live < kRows);
-        if (masked) {
+        if (__any_sync(~0u, live < kRows)) {
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
             if (i >= live) x[i] = 0xff800000u;
         }
-        float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < kRows; i += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            part[e] = fmaxf(fmaxf(part[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + 4 + e]));
-        float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-        top *= P.scale_log2;
-        const bool moved = j > 0 && __any_sync(~0u, top > m + kSlack);
-        if (j > 0 && (S::kApart || moved)) {  // the product before is complete: O may be rescaled, P written
+        if (S::kApart && j > 0) {  // the product before is complete: P may be written
           fine = await(c, &c.pv_done[t], (done - 1) & 1, a.status);
           if (!fine) break;
           tc_fence_after();
         }
-        if (j == 0) {
-          m = top;
-        } else if (moved) {
-          const float up = top > m + kSlack ? top : m, f = up > m ? ex2(m - up) : 1.f;
+        // The first half's probabilities are taken with the reference as it stands, the maximum beside them.  Where a
+        // row's maximum has outgrown the reference (always at its first keys, seldom later), what is there is brought
+        // to the maximum and the half is taken again.
+        uint64_t sum[2];
+        for (;;) {
+          float top = 0.f;
+          exponentials<T, true>(x, x + 64, P.scale_log2, m == -INFINITY ? 0.f : m, tp, sum[0], top);
+          top *= P.scale_log2;
+          const bool grown = top > m + kSlack;
+          if (!__any_sync(~0u, grown)) break;
+          const float up = grown ? top : m, f = grown ? ex2(m - up) : 1.f;  // (0 at the row's first keys)
           m = up;
-          l *= f;
+          if (j > 0) {
+            if (!S::kApart) {
+              fine = await(c, &c.pv_done[t], (done - 1) & 1, a.status);
+              if (!fine) break;
+              tc_fence_after();
+            }
+            l *= f;
 #pragma unroll
-          for (int i = 0; i < D; i += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + i, o);
-            tmem_wait_ld();
+            for (int i = 0; i < D; i += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + i, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(to + i, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(to + i, o);
+            }
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        // (a masked score's probability is an exact zero only over the MUFU)
-        l += masked ? exponentials<T, 0>(x, P.scale_log2, ref, tp, c.p_full[t], lane)
-                    : exponentials<T, S::kFma>(x, P.scale_log2, ref, tp, c.p_full[t], lane);
+        if (!fine) break;
+        announce(&c.p_full[t][0], lane);
+        float unused;
+        exponentials<T, false>(x + 64, nullptr, P.scale_log2, m == -INFINITY ? 0.f : m, tp + 32, sum[1], unused);
+        announce(&c.p_full[t][1], lane);
+        const float2 total = both(add2(sum[0], sum[1]));
+        l += total.x + total.y;
       }
       if (!fine) break;
       if (n_here > 0) {
@@ -847,8 +849,8 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
   }
 }
 
-// The pieces of one (row block, kv head) joined, a block for 32 rows of one of
-// its row tiles; launched while the first kernel runs.  The pieces' weights for
+// The pieces of a (row block, kv head) joined, 32 rows of one of its row tiles
+// at a time; launched while the first kernel runs.  The pieces' weights for
 // the rows are taken first, so that no output load waits for another.
 constexpr int kJoinRows = 32;
 
@@ -859,65 +861,67 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Promp
   __shared__ int at[6];
   __shared__ float weight[kMostPieces][kJoinRows];
   const mk_prompt_args& a = P.a;
-  const int t = blockIdx.x / PARTS % TILES, first_row = blockIdx.x % PARTS * kJoinRows, tid = threadIdx.x;
-  if (tid < 32) {
-    Walk<TILES, true> walk;
-    walk.begin(P);
-    const long long number = blockIdx.x / (PARTS * TILES);
-    const int hit = walk.find(P, number);
-    if (tid == 0) at[0] = 0;
-    __syncwarp();
-    if (tid == hit) {
-      const int r = (int)(number - walk.base - walk.before), kv_heads = a.pages.n_kv_heads;
-      at[1] = (int)(walk.slot_base + walk.slot_before) + r * walk.w.pieces;  // (r = block * kv_heads + head)
-      at[2] = r / kv_heads * TILES * P.tokens + t * P.tokens;
-      at[3] = r % kv_heads;
-      at[4] = walk.s.q0;
-      at[5] = walk.s.n;
-      at[0] = walk.w.pieces;
+  const int tid = threadIdx.x;
+  Walk<TILES, true> walk;
+  if (tid < 32) walk.begin(P);
+  for (long long number = blockIdx.x;; number += gridDim.x) {
+    const int t = number / PARTS % TILES, first_row = number % PARTS * kJoinRows;
+    if (tid < 32) {
+      const int hit = walk.find(P, number / (PARTS * TILES));
+      if (tid == 0) at[0] = 0;
+      __syncwarp();
+      if (tid == hit) {
+        const int r = (int)(number / (PARTS * TILES) - walk.base - walk.before), kv_heads = a.pages.n_kv_heads;
+        at[1] = (int)(walk.slot_base + walk.slot_before) + r * walk.w.pieces;  // (r = block * kv_heads + head)
+        at[2] = r / kv_heads * TILES * P.tokens + t * P.tokens;
+        at[3] = r % kv_heads;
+        at[4] = walk.s.q0;
+        at[5] = walk.s.n;
+        at[0] = walk.w.pieces;
+      }
     }
-  }
-  __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int pieces = at[0], slot = at[1];
-  if (pieces == 0 || slot + pieces > P.slots) return;
-  const int rows = min(kJoinRows, min(P.tokens, at[5] - at[2]) * P.group - first_row);  // (rows of tokens that exist)
-  if (rows <= 0) return;
-  const float* part = P.partial + (long long)slot * S::kPartial + t * (kRows * (D + 2));
-  // a row's weights are 2^(m_k - m) / sum_k l_k 2^(m_k - m); a piece in which the row sees no key (m_k = -inf) has
-  // weight 0 and is not read: its output may not be there
-  if (tid < rows) {
-    const float* p = part + first_row + tid;
-    float m = -INFINITY, l = 0.f;
+    __syncthreads();
+    if (number == blockIdx.x) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int pieces = at[0], slot = at[1];
+    if (pieces == 0 || slot + pieces > P.slots) return;
+    const int rows = min(kJoinRows, min(P.tokens, at[5] - at[2]) * P.group - first_row);  // (rows of tokens that exist)
+    const float* part = P.partial + (long long)slot * S::kPartial + t * (kRows * (D + 2));
+    // a row's weights are 2^(m_k - m) / sum_k l_k 2^(m_k - m); a piece in which the row sees no key (m_k = -inf) has
+    // weight 0 and is not read: its output may not be there
+    if (tid < rows) {
+      const float* p = part + first_row + tid;
+      float m = -INFINITY, l = 0.f;
 #pragma unroll 4
-    for (int k = 0; k < pieces; ++k) m = fmaxf(m, p[(long long)k * S::kPartial]);
+      for (int k = 0; k < pieces; ++k) m = fmaxf(m, p[(long long)k * S::kPartial]);
 #pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
-      const float w = m == -INFINITY ? 0.f : ex2(p[(long long)k * S::kPartial] - m);
-      weight[k][tid] = w;
-      l += w * p[(long long)k * S::kPartial + kRows];
+      for (int k = 0; k < pieces; ++k) {
+        const float w = m == -INFINITY ? 0.f : ex2(p[(long long)k * S::kPartial] - m);
+        weight[k][tid] = w;
+        l += w * p[(long long)k * S::kPartial + kRows];
+      }
+      const float inv = m == -INFINITY ? 0.f : 1.f / l;
+      for (int k = 0; k < pieces; ++k) weight[k][tid] *= inv;
     }
-    const float inv = m == -INFINITY ? 0.f : 1.f / l;
-    for (int k = 0; k < pieces; ++k) weight[k][tid] *= inv;
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll
-  for (int i0 = 0; i0 < kJoinRows * LANES; i0 += 256) {
-    const int i = i0 + tid, r = i / LANES, c = i % LANES * 4;
-    if (r >= rows) continue;
-    const float* p = part + 2 * kRows + (first_row + r) * D + c;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < kJoinRows * LANES; i0 += 256) {
+      const int i = i0 + tid, r = i / LANES, c = i % LANES * 4;
+      if (r >= rows) continue;
+      const float* p = part + 2 * kRows + (first_row + r) * D + c;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
-      const float w = weight[k][r];
-      if (w == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(p + (long long)k * S::kPartial);
-      o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      for (int k = 0; k < pieces; ++k) {
+        const float w = weight[k][r];
+        if (w == 0.f) continue;
+        const float4 v = *reinterpret_cast<const float4*>(p + (long long)k * S::kPartial);
+        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      }
+      const int row = first_row + r;
+      T* out = static_cast<T*>(a.out) + (long long)(at[4] + at[2] + row / P.group) * a.o_row_stride +
+               (long long)(at[3] * P.group + row % P.group) * a.o_head_stride + c;
+      *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
     }
-    const int row = first_row + r;
-    T* out = static_cast<T*>(a.out) + (long long)(at[4] + at[2] + row / P.group) * a.o_row_stride +
-             (long long)(at[3] * P.group + row % P.group) * a.o_head_stride + c;
-    *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
+    __syncthreads();  // (at and the weights are done with)
   }
 }
 
@@ -942,11 +946,11 @@ mk_status launch(PromptParams& P, cudaStream_t s, std::string& err) {
   P.sms = dev.sms;
   long long items = items_of<D, TILES>(P.a);
   const long long keys = g.page_table ? (long long)g.table_width * g.page_size : g.page_size;
-  const long long slots = std::min<long long>(4 * dev.sms, P.a.workspace_bytes / (S::kPartial * sizeof(float)));
-  if (P.a.workspace && slots >= 4 * dev.sms && may_cut(items, keys, dev.sms)) {
+  const long long slots = std::min<long long>(kSlots * dev.sms, P.a.workspace_bytes / (S::kPartial * sizeof(float)));
+  if (P.a.workspace && slots >= kSlots * dev.sms && may_cut(items, keys, dev.sms)) {
     P.partial = static_cast<float*>(P.a.workspace);
     P.slots = (int)slots;
-    items += 2 * dev.sms;  // pieces: at most tiles / piece_tiles + 1 each, blocks * tiles <= 2 total
+    items += 2 * kShares * dev.sms;  // pieces: at most tiles / piece_tiles + 1 each, blocks * tiles <= 2 total
   }
   if (items > 0x7fffffffll) {
     err = "too many row tiles for one launch";
@@ -956,7 +960,7 @@ mk_status launch(PromptParams& P, cudaStream_t s, std::string& err) {
   e = cudaGetLastError();
   if (e != cudaSuccess || !P.partial) return cuda_result(e, "mk_prompt_attention launch", err);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(slots / 2 * TILES * (kRows / kJoinRows)));  // (a joined block has two pieces or more)
+  cfg.gridDim = dim3(4 * dev.sms);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -981,7 +985,7 @@ size_t prompt_workspace_bytes(int batch, int n_tokens, int n_q_heads, int n_kv_h
   a.pages.n_kv_heads = n_kv_heads;
   const bool small = head_dim <= 64;
   if (!may_cut(small ? items_of<64, kTiles64>(a) : items_of<128, 2>(a), max_keys, dev.sms)) return 0;
-  return (size_t)4 * dev.sms * (small ? Shape<64, kTiles64>::kPartial : Shape<128, 2>::kPartial) * sizeof(float);
+  return (size_t)kSlots * dev.sms * (small ? Shape<64, kTiles64>::kPartial : Shape<128, 2>::kPartial) * sizeof(float);
 }
 
 mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err) {

@@ -81,7 +81,7 @@ def test_append_refuses(path, value, status):
     ("n_q_heads", 2 * 129, UNSUPPORTED), ("causal", 2, INVALID), ("scale", -1.0, INVALID), ("scale", math.inf, INVALID),
     ("scale", math.nan, INVALID), ("q", 0, INVALID), ("out", A + 4, INVALID), ("q_row_stride", 7, INVALID),
     ("cu_q", 0, INVALID), ("kv_lens", 0, INVALID), ("pages.page_size", 48, UNSUPPORTED),
-    ("pages.page_size", 8, UNSUPPORTED), ("pages.page_table", 0, INVALID)])
+    ("pages.page_size", 8, UNSUPPORTED), ("pages.page_table", 0, INVALID), ("workspace", A + 64, WORKSPACE)])
 def test_prompt_refuses(path, value, status):
     refused(mk.mk_prompt_attention, prompt_args(), path, value, status)
 
