@@ -2,16 +2,17 @@
 // grammar's mask on logits, and the choice of the largest.
 //
 // One row is the work of one thread-block cluster; each of its blocks takes a
-// range of the vocabulary.  First a block marks in shared memory, a word per id
-// of its range, how often the id stands in the row's history (integer atomics,
-// so their order does not matter) and whether the bias list names it; then it
-// streams its logits once, the first of them loaded before the marks are made.
-// Nothing but logits, history, bias list and mask bits is read, and no count
-// ever exists in device memory.  A mark leads to its id's
-// entry of the bias list; for an id that the list names twice the sum is taken
-// from the list, in its order, by the thread that has the id.  The blocks' best (value, id) keys meet
-// in the first block through distributed shared memory: no workspace, no
-// atomics on device memory, one launch.
+// range of the vocabulary.  First a block marks in shared memory, 16 bits per
+// id of its range, how often the id stands in the row's history (integer
+// atomics, so their order does not matter) and whether the bias list names it;
+// then it streams its logits once, the first of them loaded before the marks
+// are made.  Ids with a bias, few, pass unchanged there and are seen to
+// afterwards by the list's entries, each id by one of them; where the list
+// names an id twice, its values add up in list order.  Nothing but logits,
+// history, bias list and mask bits is read, and no count ever exists in device
+// memory.  The blocks' best (value, id) keys meet in the first block through
+// distributed shared memory: no workspace, no atomics on device memory, one
+// launch.
 //
 // Bound: memory (logits in, logits out) for a batch; for a single row the
 // latency of its dependent steps (lengths, history, logits, cluster barrier).
@@ -27,14 +28,21 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kPer = 8;                  // ids a thread has in flight
-constexpr int kThreads = 512;
-constexpr int kMaxTile = 16384;          // ids marked at a time: 64 KB of marks, so that an SM holds two blocks
-// The mark of an id.  Bit 0: it stands in the history; from bit 1: its
-// occurrences in the answer; kBias: the bias list names it, kTwice: more than
-// once.  The entry's place in the row's list lies in bits 14-29 as long as
-// history and list are short enough for that, else (WIDE) in a second word.
-constexpr uint32_t kBias = 1u << 30, kTwice = 1u << 31;
-constexpr int kPlaceBit = 14, kShortHistory = (1 << 13) - 1, kShortList = 1 << 16;
+constexpr int kThreads = 1024;
+constexpr int kMarkBytes = 128 * 1024;   // marks of the ids that a block takes at a time
+// The mark of an id (M: 16 bits, or 32 for a history above kShortHistory ids).
+// Bit 0: it stands in the history; from bit 1: its occurrences in the answer;
+// the two highest: the bias list names it, and more than once.
+constexpr int kShortHistory = (1 << 13) - 1;
+template <class M>
+struct Mark {
+  static constexpr int kBits = 8 * sizeof(M), kPerWord = 32 / kBits;
+  static constexpr uint32_t kBias = 1u << (kBits - 2), kTwice = 1u << (kBits - 1), kCounts = kBias - 1;
+  // the word that holds the mark of id `at`, and the mark's place in it
+  static __device__ __forceinline__ int shift(unsigned at) { return sizeof(M) == 2 ? (at & 1) * 16 : 0; }
+  static __device__ __forceinline__ uint32_t* word(uint32_t* marks, unsigned at) { return marks + at / kPerWord; }
+  static __device__ __forceinline__ uint32_t get(const uint32_t* marks, unsigned at) { return reinterpret_cast<const M*>(marks)[at]; }
+};
 
 template <class T>
 __device__ __forceinline__ float to_f32(T v) { return static_cast<float>(v); }
@@ -71,7 +79,7 @@ struct Batch {
 };
 
 // The row's bias values with this id, added in list order by a warp.
-__device__ __forceinline__ float sum_of_id(const mk_logits_args& a, int b0, int b1, int id) {
+__device__ __noinline__ float sum_of_id(const mk_logits_args& a, int b0, int b1, int id) {
   float sum = 0.f;
 #pragma unroll 2
   for (int i = b0 + (int)(threadIdx.x & 31); i - (int)(threadIdx.x & 31) < b1; i += 32) {
@@ -82,13 +90,12 @@ __device__ __forceinline__ float sum_of_id(const mk_logits_args& a, int b0, int 
   return sum;
 }
 
-template <class T, bool VEC, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_constant__ mk_logits_args a, int per_block, int tile) {
+template <class T, bool VEC, class M>
+__global__ void __launch_bounds__(kThreads, 1) logits_kernel(const __grid_constant__ mk_logits_args a, int per_block, int tile) {
   using B = Batch<T, VEC>;
+  using K = Mark<M>;
   constexpr int NT = kThreads;
-  constexpr uint32_t kCounts = WIDE ? kBias - 1 : (1u << kPlaceBit) - 1;
-  extern __shared__ __align__(16) uint32_t marks[];  // [tile]
-  uint32_t* const place = marks + tile;              // WIDE: [tile]
+  extern __shared__ __align__(16) uint32_t marks[];  // [tile] of M
   __shared__ unsigned long long best_key[NT / 32 + 1];
   cg::cluster_group cluster = cg::this_cluster();
   const int row = blockIdx.y, tid = threadIdx.x;
@@ -104,18 +111,19 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
   // the first ids of the history, before its length is known (a row holds history_width ids)
   const bool penalised = a.repetition || a.frequency || a.presence;
   const int* history = a.history + (a.history ? row * a.history_stride : 0);
-  int id[8];
+  int id[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) id[e] = penalised && tid + e * NT < a.history_width ? __ldg(history + tid + e * NT) : -1;
+  for (int e = 0; e < 4; ++e) id[e] = penalised && tid + e * NT < a.history_width ? __ldg(history + tid + e * NT) : -1;
 
   int len = 0, first = 0, b0 = 0, b1 = 0;
-  float rep = 1.f, freq = 0.f, pres = 0.f;
+  float rep = 1.f, inv_rep = 1.f, freq = 0.f, pres = 0.f;
   if (penalised) {
     len = a.history_lens ? __ldg(a.history_lens + row) : a.history_width;
     first = a.prompt_lens ? __ldg(a.prompt_lens + row) : 0;
     if (a.repetition) rep = __ldg(a.repetition + row);
     if (a.frequency) freq = __ldg(a.frequency + row);
     if (a.presence) pres = __ldg(a.presence + row);
+    inv_rep = 1.f / rep;
   }
   if (a.bias_indptr) {
     b0 = __ldg(a.bias_indptr + row);
@@ -131,35 +139,41 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
   }
   const bool marked = len > 0 || b1 > b0;
 
+  // x after the penalties that a mark asks for
+  auto penalise = [&](float v, uint32_t mark) {
+    const uint32_t c = mark & K::kCounts;
+    const float scaled = v > 0.f ? v * inv_rep : v * rep;
+    v = c ? scaled : v;
+    return c > 1 ? v - freq * (float)(c >> 1) - pres : v;
+  };
   float best_value = -INFINITY;
   int best_id = -1;
   for (int lo = block_lo; lo < block_hi; lo += tile) {
     const int n = min(tile, block_hi - lo);
     if (lo != block_lo) B::load(x, src + lo, n);
     if (marked) {
-      if (lo != block_lo) __syncthreads();  // (the marks of the tile before are done with)
-      for (int i = tid; i < (n + 3) / 4; i += NT) reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < (n + 4 * K::kPerWord - 1) / (4 * K::kPerWord); i += NT) reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
-      for (int i0 = tid; i0 < len; i0 += 8 * NT) {  // (8 loads in flight a thread)
-        if (len > 8 * NT && (i0 != tid || lo != block_lo)) {
+      for (int i0 = tid; i0 < len; i0 += 4 * NT) {  // (4 loads in flight a thread)
+        if (len > 4 * NT && (i0 != tid || lo != block_lo)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) id[e] = i0 + e * NT < len ? __ldg(history + i0 + e * NT) : -1;
+          for (int e = 0; e < 4; ++e) id[e] = i0 + e * NT < len ? __ldg(history + i0 + e * NT) : -1;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) {
           const unsigned at = (unsigned)id[e] - (unsigned)lo;
           if (id[e] >= 0 && at < (unsigned)n && i0 + e * NT < len) {
-            if (i0 + e * NT >= first) atomicAdd(marks + at, 2u);
-            else atomicOr(marks + at, 1u);
+            if (i0 + e * NT >= first) atomicAdd(K::word(marks, at), 2u << K::shift(at));
+            else atomicOr(K::word(marks, at), 1u << K::shift(at));
           }
         }
       }
       for (int i = b0 + tid; i < b1; i += NT) {
-        const int id = __ldg(a.bias_ids + i);
-        const unsigned at = (unsigned)id - (unsigned)lo;
-        if (id >= 0 && at < (unsigned)n) {
-          if (WIDE) place[at] = i - b0;
-          if (atomicOr(marks + at, WIDE ? kBias : kBias | (uint32_t)(i - b0) << kPlaceBit) & kBias) atomicOr(marks + at, kTwice);
+        const int which = __ldg(a.bias_ids + i);
+        const unsigned at = (unsigned)which - (unsigned)lo;
+        if (which >= 0 && at < (unsigned)n) {
+          const uint32_t old = atomicOr(K::word(marks, at), K::kBias << K::shift(at));
+          if (old >> K::shift(at) & K::kBias) atomicOr(K::word(marks, at), K::kTwice << K::shift(at));
         }
       }
       __syncthreads();
@@ -170,53 +184,44 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < kPer; ++j) y[j] = x[j];
       if (left > B::kIds) B::load(x, src + base + B::kIds, left - B::kIds);  // the next batch, while this one is worked on
-      uint32_t allowed[VEC ? kPer / 4 : kPer];  // (lo is a multiple of 128: four ids from a multiple of 4 share a word)
-      if (mask) {
-#pragma unroll
-        for (int j = 0; j < kPer; j += VEC ? 4 : 1) allowed[VEC ? j / 4 : j] = B::at(j) < left ? __ldg(mask + ((base + B::at(j)) >> 5)) : 0u;
-      }
 #pragma unroll
       for (int g = 0; g < kPer / 4; ++g) {
-        uint32_t mark[4] = {0, 0, 0, 0};
-        if (marked) {
-          if (VEC) {  // (one 16-byte read: four ids in a row a lane, no bank twice)
-            if (B::at(4 * g) < left) *reinterpret_cast<uint4*>(mark) = *reinterpret_cast<const uint4*>(marks + done + B::at(4 * g));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mark[e] = B::at(4 * g + e) < left ? marks[done + B::at(4 * g + e)] : 0u;
-          }
-        }
-        float twice[4] = {0.f, 0.f, 0.f, 0.f};
-        if (__any_sync(~0u, (mark[0] | mark[1] | mark[2] | mark[3]) & kTwice)) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int mine = base + B::at(4 * g + e);
-            for (unsigned need = __ballot_sync(~0u, mark[e] & kTwice); need; need &= need - 1) {
-              const float sum = sum_of_id(a, b0, b1, __shfl_sync(~0u, mine, __ffs(need) - 1));
-              if ((tid & 31) == __ffs(need) - 1) twice[e] = sum;
+        uint32_t mark[4] = {0, 0, 0, 0}, allowed[4] = {1, 1, 1, 1};
+        if (VEC) {  // (lo is a multiple of 128: four ids from a multiple of 4 share a mask word)
+          const int at = B::at(4 * g);
+          if (marked && at < left) {
+            if constexpr (sizeof(M) == 4) {
+              *reinterpret_cast<uint4*>(mark) = *reinterpret_cast<const uint4*>(marks + done + at);
+            } else {
+              const uint2 two = *reinterpret_cast<const uint2*>(marks + (done + at) / 2);
+              mark[0] = two.x & 0xffff, mark[1] = two.x >> 16, mark[2] = two.y & 0xffff, mark[3] = two.y >> 16;
             }
           }
+          if (mask) {
+            const uint32_t word = at < left ? __ldg(mask + ((base + at) >> 5)) >> ((base + at) & 31) : 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) allowed[e] = word >> e & 1;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = B::at(4 * g + e);
+            if (marked && at < left) mark[e] = K::get(marks, done + at);
+            if (mask) allowed[e] = at < left ? __ldg(mask + ((base + at) >> 5)) >> ((base + at) & 31) & 1 : 0u;
+          }
+        }
+        if (mark[0] | mark[1] | mark[2] | mark[3]) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(mark[e] & K::kBias)) y[4 * g + e] = penalise(y[4 * g + e], mark[e]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 4 * g + e, at = B::at(j);
-          float v = y[j];
-          if (mark[e]) {
-            const uint32_t c = mark[e] & kCounts;
-            if (c) {
-              if (a.repetition) v = v > 0.f ? v / rep : v * rep;
-              if (c > 1) v = v - freq * (float)(c >> 1) - pres;
-            }
-            if (mark[e] & kTwice) {
-              v += twice[e];
-            } else if (mark[e] & kBias) {
-              v += __ldg(a.bias_values + b0 + (WIDE ? place[done + at] : mark[e] >> kPlaceBit & (kShortList - 1)));
-            }
-          }
-          if (mask && !(allowed[VEC ? g : j] >> ((base + at) & 31) & 1)) v = -INFINITY;
-          y[j] = v;
-          if (v > best_value && at < left) {  // (a thread's ids ascend: the lowest of equal ones stays; NaN and -inf never win)
-            best_value = v;
+          const bool later = mark[e] & K::kBias;
+          if (!allowed[e] && !later) y[j] = -INFINITY;
+          if (y[j] > best_value && !later && at < left) {  // (a thread's ids ascend: the lowest of equal ones stays; NaN and -inf never win)
+            best_value = y[j];
             best_id = base + at;
           }
         }
@@ -234,6 +239,31 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
         }
       }
     }
+    if (b1 > b0) {
+      // ---- ids with a bias, each by the first entry that takes its mark off (whole warps come here)
+      __syncthreads();  // (their values as they were are written by now)
+      for (int i = b0 + tid; i - (tid & 31) < b1; i += NT) {
+        const int which = i < b1 ? __ldg(a.bias_ids + i) : -1;
+        const unsigned at = (unsigned)which - (unsigned)lo;
+        uint32_t mark = 0;
+        if (which >= 0 && at < (unsigned)n) mark = atomicAnd(K::word(marks, at), ~(K::kBias << K::shift(at))) >> K::shift(at);
+        const bool mine = mark & K::kBias;
+        float add = mine && !(mark & K::kTwice) ? __ldg(a.bias_values + i) : 0.f;
+        for (unsigned need = __ballot_sync(~0u, mine && (mark & K::kTwice)); need; need &= need - 1) {
+          const float sum = sum_of_id(a, b0, b1, __shfl_sync(~0u, which, __ffs(need) - 1));
+          if ((tid & 31) == __ffs(need) - 1) add = sum;
+        }
+        if (!mine) continue;
+        float v = penalise(to_f32(src[which]), mark) + add;
+        if (mask && !(__ldg(mask + (which >> 5)) >> (which & 31) & 1)) v = -INFINITY;
+        if (dst) dst[which] = v;
+        if (v > best_value || (v == best_value && which < best_id)) {
+          best_value = v;
+          best_id = which;
+        }
+      }
+    }
+    if (marked && lo + tile < block_hi) __syncthreads();  // (the marks are cleared for the next tile)
   }
   if (!a.next_tokens) return;
   unsigned long long best = best_id >= 0 ? argmax_key(best_value + 0.f, best_id) : 0;  // (-0 ties with 0)
@@ -266,16 +296,16 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
   cluster.sync();  // no block leaves while its key may still be read
 }
 
-template <class T, bool VEC, bool WIDE>
+template <class T, bool VEC, class M>
 mk_status launch(const mk_logits_args& a, int cluster, const Device& dev, cudaStream_t s, std::string& err) {
-  cudaError_t e = allow<logits_kernel<T, VEC, WIDE>>(dev, kMaxTile * 8, true);
+  cudaError_t e = allow<logits_kernel<T, VEC, M>>(dev, kMarkBytes, true);
   if (e != cudaSuccess) return cuda_result(e, "mk_process_logits attributes", err);
   const int per_block = ((a.vocab - 1) / cluster + 128) / 128 * 128;
-  const int tile = std::min(per_block, kMaxTile);
+  const int tile = std::min<int>(per_block, kMarkBytes / sizeof(M));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, a.rows);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.history || a.bias_indptr ? tile * (WIDE ? 8 : 4) : 0;
+  cfg.dynamicSmemBytes = a.history || a.bias_indptr ? tile * sizeof(M) : 0;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -284,11 +314,11 @@ mk_status launch(const mk_logits_args& a, int cluster, const Device& dev, cudaSt
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_result(cudaLaunchKernelEx(&cfg, logits_kernel<T, VEC, WIDE>, a, per_block, tile), "mk_process_logits launch", err);
+  return cuda_result(cudaLaunchKernelEx(&cfg, logits_kernel<T, VEC, M>, a, per_block, tile), "mk_process_logits launch", err);
 }
 
-// Blocks of a row (a cluster): enough for two on each SM, as long as each has 2048 ids or more.  A cluster lies within
-// one group of SMs: of 16 blocks hardly one fits a group, so 16 is for one to four rows.
+// Blocks of a row (a cluster): one for each SM, as long as each has 2048 ids or more.  A cluster lies within one group
+// of SMs: of 16 blocks hardly one fits a group, so 16 is for one to four rows.
 template <class T, bool VEC>
 mk_status size_up(const mk_logits_args& a, cudaStream_t s, std::string& err) {
   Device dev;
@@ -296,9 +326,9 @@ mk_status size_up(const mk_logits_args& a, cudaStream_t s, std::string& err) {
   if (e != cudaSuccess) return cuda_result(e, "mk_process_logits device query", err);
   const int most = a.rows <= 4 ? 16 : 8;
   int cluster = 1;
-  while (cluster < most && a.vocab > 2048 * cluster && (long long)a.rows * cluster * 2 < dev.sms * 3) cluster *= 2;
-  if (a.history_width > kShortHistory || a.bias_count > kShortList) return launch<T, VEC, true>(a, cluster, dev, s, err);
-  return launch<T, VEC, false>(a, cluster, dev, s, err);
+  while (cluster < most && a.vocab > 2048 * cluster && (long long)a.rows * cluster * 2 <= dev.sms) cluster *= 2;
+  if (a.history_width > kShortHistory) return launch<T, VEC, uint32_t>(a, cluster, dev, s, err);
+  return launch<T, VEC, uint16_t>(a, cluster, dev, s, err);
 }
 
 template <class T>

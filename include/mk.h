@@ -545,7 +545,7 @@ typedef struct mk_paged_attn_args {
  * history[b][0 .. history_lens[b]) and s(v) those from prompt_lens[b] on (the
  * answer so far), in this order and in fp32:
  *   x = logits[b][v]
- *   if n(v) > 0:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   if n(v) > 0:  x = x > 0 ? x * (1 / repetition[b]) : x * repetition[b]
  *   x = x - frequency[b] * s(v) - presence[b] * (s(v) > 0)
  *   x = x + sum of the row's bias values with this id
  *   x = -infinity where the mask's bit v is 0, whatever x was

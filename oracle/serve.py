@@ -66,14 +66,13 @@ def process(logits, history=None, history_lens=None, prompt_lens=None, repetitio
         if history is not None:
             n = history.shape[1] if history_lens is None else min(max(int(history_lens[r]), 0), history.shape[1])
             first = 0 if prompt_lens is None else int(prompt_lens[r])
-            every, said = [0] * V, [0] * V
-            for i in range(n):
-                v = int(history[r, i])
+            every, said = {}, {}
+            for i, v in enumerate(history[r, :n].tolist()):
                 if 0 <= v < V:
-                    every[v] += 1
-                    said[v] += i >= first
-            for v in range(V):
-                if every[v] and repetition is not None:
+                    every[v] = every.get(v, 0) + 1
+                    said[v] = said.get(v, 0) + (i >= first)
+            for v in every:
+                if repetition is not None:
                     rep = float(repetition[r])
                     x[r, v] = x[r, v] / rep if x[r, v] > 0 else x[r, v] * rep
                 if said[v]:
@@ -84,13 +83,12 @@ def process(logits, history=None, history_lens=None, prompt_lens=None, repetitio
                 if 0 <= int(bias[1][i]) < V:
                     x[r, int(bias[1][i])] += float(bias[2][i])
         if mask is not None:
-            row = mask[r if mask.shape[0] > 1 else 0]
-            for v in range(V):
-                if not (int(row[v // 32]) >> (v % 32)) & 1:
-                    x[r, v] = -math.inf
+            row = mask[r if mask.shape[0] > 1 else 0].long()
+            bits = (row[:, None] >> torch.arange(32)) & 1  # bit v % 32 of word v // 32
+            x[r, bits.reshape(-1)[:V] == 0] = -math.inf
         choice, top = -1, -math.inf
-        for v in range(V):
-            if float(x[r, v]) > top:  # (a NaN is never larger)
-                choice, top = v, float(x[r, v])
+        for v, value in enumerate(x[r].tolist()):
+            if value > top:  # (a NaN is never larger)
+                choice, top = v, value
         best.append(choice)
     return x, torch.tensor(best, dtype=torch.int32)

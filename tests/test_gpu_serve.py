@@ -524,6 +524,10 @@ def check_logits(got, best, logits, kw):
     (2, 20011, torch.float32, 1000, 70, True),
     (1, 40000, BF, 33, 33, False),
     (70, 2051, HF, 17, 5, True),
+    (2, 3000, torch.float32, 9000, 50, True),       # a history too long for the short marks
+    (80, 70001, BF, 40, 40, True),                  # a row in one block, in two parts
+    (80, 70004, torch.float32, 40, 40, False),
+    (1, 90000, torch.float32, 12000, 3000, True),   # the long marks, in parts; a list with many ids twice
 ])
 def test_logits(R, V, dtype, H, bias, mask):
     logits, kw = logits_case(R, V, dtype, H, bias, mask)
