@@ -96,32 +96,28 @@ __device__ __forceinline__ int keys_of(const mk_paged_attn_args& a, int b) {
   return n;
 }
 
-// The units of all sequences end to end, and where unit `u` or sequence `b` lies among them.
-// Called by the whole block of NT threads; `scratch` holds NT + 1 sums.
-struct Layout {
-  long long total;
-  long long before;  // units before the sequence asked for
-  int b;
-};
+// The units of all sequences end to end (below 2^31: the launch sees to that).
+// Called by a whole block of NT threads, each of which counts `per` sequences;
+// `scratch` receives the units before each thread's, and the total last.
 template <int NT>
-__device__ __forceinline__ long long scan_units(const PagedParams& P, long long* scratch, int& per) {
+__device__ __forceinline__ int scan_units(const PagedParams& P, int* scratch, int& per) {
   const int B = P.a.batch, pairs = P.a.pages.n_kv_heads * P.tiles;
   per = (B + NT - 1) / NT;
-  long long mine = 0;
+  int mine = 0;
   for (int b = threadIdx.x * per; b < min(B, (int)(threadIdx.x + 1) * per); ++b)
-    mine += (long long)((keys_of(P.a, b) + kUnit - 1) / kUnit) * pairs;
+    mine += (keys_of(P.a, b) + kUnit - 1) / kUnit * pairs;
   // exclusive sums over the block
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long sum = mine;
+  int sum = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(~0u, sum, d);
+    const int o = __shfl_up_sync(~0u, sum, d);
     if (lane >= d) sum += o;
   }
-  __shared__ long long warp_sum[NT / 32];
+  __shared__ int warp_sum[NT / 32];
   if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
-  long long base = 0, total = 0;
+  int base = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) base += warp_sum[w];
@@ -132,6 +128,17 @@ __device__ __forceinline__ long long scan_units(const PagedParams& P, long long*
   __syncthreads();
   return total;
 }
+
+// Block c's share of `total` units: equal shares, the first total % n of them one unit longer.
+struct Shares {
+  int base, longer;
+  __device__ __forceinline__ Shares(int total, int n) : base(total / n), longer(total - total / n * n) {}
+  __device__ __forceinline__ int begin(int c) const { return c * base + min(c, longer); }
+  __device__ __forceinline__ int of(int unit) const {  // the share that holds a unit
+    const int cut = longer * (base + 1);
+    return unit < cut ? unit / (base + 1) : longer + (unit - cut) / base;
+  }
+};
 
 // One pair's place in the flattened order: sequence b, head tile h (kv head * tiles + tile).
 struct Walk {
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);  // (the swizzle goes by address)
   __shared__ uint64_t landed[kWarps][S::kStages];
-  __shared__ long long scratch[kThreads + 1];
+  __shared__ int scratch[kThreads + 1];
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quad = lane >> 2, sub = lane & 3;
@@ -182,9 +189,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
   const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kPiece;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (TMA && tid == 0) {
+    prefetch_map(&P.tk);
+    prefetch_map(&P.tv);
+  }
   int per;
-  const long long total = scan_units<kThreads>(P, scratch, per);
-  const long long u0 = total * blockIdx.x / P.n_cta, u1 = total * (blockIdx.x + 1) / P.n_cta;
+  const int total = scan_units<kThreads>(P, scratch, per);
+  const Shares shares(total, P.n_cta);
+  const int u0 = shares.begin(blockIdx.x), u1 = shares.begin(blockIdx.x + 1);
   if (u0 >= u1) return;
 
   Walk load;
@@ -196,18 +208,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
       if (scratch[mid] <= u0) lo = mid;
       else hi = mid - 1;
     }
-    long long at = scratch[lo];
+    int at = scratch[lo];
     const int pairs = P.a.pages.n_kv_heads * P.tiles;
     load.enter(P, lo * per);
-    while (at + (long long)load.ntile * pairs <= u0) {
-      at += (long long)load.ntile * pairs;
+    while (at + load.ntile * pairs <= u0) {
+      at += load.ntile * pairs;
       load.enter(P, load.b + 1);
     }
-    load.h = (int)((u0 - at) / load.ntile);
-    load.tile = (int)((u0 - at) % load.ntile);
+    load.h = (u0 - at) / load.ntile;
+    load.tile = (u0 - at) % load.ntile;
   }
   Walk use = load;
-  const int n_units = (int)(u1 - u0);
+  const int n_units = u1 - u0;
 
   // The piece that is loaded next, its page looked up one unit ahead.  A piece holds its keys' 16 rows, then its
   // values', each as halves of 64 dimensions: 128 bytes a row, 16-byte chunks swizzled by the row's low three bits.
@@ -525,82 +537,85 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
 
 // The parts of one (sequence, query head) joined.  Launched while the first
 // kernel runs (programmatic dependent launch): it finds its place among the
-// shares, then waits for the parts.  Their weights are taken first, one part a
-// thread, so that the outputs' loads do not wait for one another.
+// shares, then waits for the parts.  A thread takes every GROUPS-th part, four
+// at a time so that their loads travel together, and keeps a running maximum.
 constexpr int kJoinThreads = 128;
 
 template <class T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ PagedParams P) {
   using S = Shape<D>;
   constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;  // threads of a part's row, 4 values each
-  __shared__ long long scratch[kJoinThreads + 1];
-  __shared__ int where[kMaxCtas];
-  __shared__ float weight[kMaxCtas], red[kJoinThreads / 32];
-  __shared__ float4 acc[GROUPS][LANES];
+  __shared__ int scratch[kJoinThreads + 1];
+  __shared__ float4 group_o[GROUPS][LANES];
+  __shared__ float group_m[GROUPS], group_l[GROUPS];
   const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   int per;
-  const long long total = scan_units<kJoinThreads>(P, scratch, per);
+  const int total = scan_units<kJoinThreads>(P, scratch, per);
   T* out = static_cast<T*>(P.a.out) + b * P.a.o_row_stride + head * P.a.o_head_stride;
   const int ntile = (keys_of(P.a, b) + kUnit - 1) / kUnit;
   const int pairs = P.a.pages.n_kv_heads * P.tiles;
-  long long at = scratch[b / per];
-  for (int i = b / per * per; i < b; ++i) at += (long long)((keys_of(P.a, i) + kUnit - 1) / kUnit) * pairs;
+  int at = scratch[b / per];
+  for (int i = b / per * per; i < b; ++i) at += (keys_of(P.a, i) + kUnit - 1) / kUnit * pairs;
   const int in_group = head % P.group, row = in_group % kRows;
-  const long long p0 = at + (long long)((head / P.group) * P.tiles + in_group / kRows) * ntile, p1 = p0 + ntile;
-  // block c's share is [total c / n, total (c + 1) / n): unit u is in share ((u + 1) n - 1) / total
-  const int c0 = ntile ? (int)(((p0 + 1) * P.n_cta - 1) / total) : 0, c1 = ntile ? (int)((p1 * P.n_cta - 1) / total) : 0;
-  const int n = c1 - c0 + 1;
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const long long u0 = total * (c0 + i) / P.n_cta, u1 = total * (c0 + i + 1) / P.n_cta;
-    where[i] = u0 < u1 ? (c0 + i) * 2 + (u0 < p0 ? 1 : 0) : -1;  // (an empty share has no part)
-  }
+  const int p0 = at + ((head / P.group) * P.tiles + in_group / kRows) * ntile;
+  const Shares shares(total, P.n_cta);
+  const int c0 = ntile ? shares.of(p0) : 0, c1 = ntile ? shares.of(p0 + ntile - 1) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (ntile == 0) {
     if (tid < D) out[tid] = static_cast<T>(0.f);
     return;
   }
-  if (n == 1) return;  // one block had it all and wrote it
-  float m = -INFINITY;
-  for (int i = tid; i < n; i += kJoinThreads) {
-    weight[i] = where[i] < 0 ? -INFINITY : P.partial[(long long)where[i] * S::kPartial + row];
-    m = fmaxf(m, weight[i]);
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-  if ((tid & 31) == 0) red[tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
-  __syncthreads();
-  float l = 0.f;
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const float w = exp2f(weight[i] - m);
-    weight[i] = w;
-    if (where[i] >= 0) l += w * P.partial[(long long)where[i] * S::kPartial + kRows + row];
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-  if ((tid & 31) == 0) red[tid >> 5] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w];
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c0 == c1) return;  // one block had it all and wrote it
   const int g = tid / LANES, c = tid % LANES;
-#pragma unroll 4
-  for (int i = g; i < n; i += GROUPS) {
-    if (where[i] < 0) continue;
-    const float4 v = *reinterpret_cast<const float4*>(P.partial + (long long)where[i] * S::kPartial + 2 * kRows + row * D + 4 * c);
-    const float w = weight[i];
-    o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = c0 + g; k0 <= c1; k0 += 4 * GROUPS) {
+    float pm[4], pl[4];
+    float4 po[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = k0 + e * GROUPS;
+      pm[e] = -INFINITY;
+      pl[e] = 0.f;
+      po[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k <= c1) {
+        // a share that begins before the pair ends with its part of it
+        const float* part = P.partial + ((long long)k * 2 + (shares.begin(k) < p0 ? 1 : 0)) * S::kPartial;
+        pm[e] = part[row];
+        pl[e] = part[kRows + row];
+        po[e] = *reinterpret_cast<const float4*>(part + 2 * kRows + row * D + 4 * c);
+      }
+    }
+    const float up = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m), f = exp2f(m - up);
+    l *= f;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w = exp2f(pm[e] - up);
+      l += w * pl[e];
+      o.x += w * po[e].x, o.y += w * po[e].y, o.z += w * po[e].z, o.w += w * po[e].w;
+    }
+    m = up;
   }
-  acc[g][c] = o;
+  if (c == 0) {
+    group_m[g] = m;
+    group_l[g] = l;
+  }
+  group_o[g][c] = o;
   __syncthreads();
   if (g == 0) {
+    float top = m;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, group_m[i]);
+    float f = exp2f(m - top);
+    l *= f;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
     for (int i = 1; i < GROUPS; ++i) {
-      const float4 v = acc[i][c];
-      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+      const float4 v = group_o[i][c];
+      f = exp2f(group_m[i] - top);
+      l += f * group_l[i];
+      o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
     }
     const float inv = 1.f / l;
     *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
@@ -653,6 +668,11 @@ mk_status launch_paged(const mk_paged_attn_args& a, void* stream, std::string& e
   P.a = a;
   P.group = a.n_q_heads / a.pages.n_kv_heads;
   P.tiles = (P.group + kRows - 1) / kRows;
+  const long long units = ((long long)a.pages.table_width * a.pages.page_size + kUnit - 1) / kUnit;
+  if (units * a.batch * a.pages.n_kv_heads * P.tiles > 0x7fffffffll) {
+    err = "batch, heads and page table reach 2^31 units of 64 keys";
+    return MK_ERR_UNSUPPORTED;
+  }
   const float scale = a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)a.pages.head_dim);
   P.scale_log2 = scale * 1.4426950408889634f;
   P.partial = static_cast<float*>(a.workspace);

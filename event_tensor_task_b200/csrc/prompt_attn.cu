@@ -416,6 +416,11 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 32) {
+    prefetch_map(&P.tq);
+    prefetch_map(&P.tk);
+    prefetch_map(&P.tv);
+  }
   if (tid == 0) {
     c.abort = 0;
     mbar_init(&c.q_full, 1);
