@@ -16,6 +16,9 @@
 //
 // Bound: memory (logits in, logits out) for a batch; for a single row the
 // latency of its dependent steps (lengths, history, logits, cluster barrier).
+// Measured (one B200, in a graph): 64 rows of 128,256 with 4,096 ids of
+// history, 64 biases and a mask each in 20 us (the stream alone 9.6: the marks
+// are made before it and hardly overlap it); one row with 1,500 ids in 5.8 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

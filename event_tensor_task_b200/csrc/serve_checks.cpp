@@ -13,6 +13,8 @@ mk_status bad(std::string& err, const std::string& what) {
   return MK_ERR_INVALID_ARG;
 }
 
+constexpr long long kMaxKeys = 0x7ffffc00;  // a tile that begins before the last key stays below 2^31
+
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 
@@ -49,8 +51,9 @@ mk_status check_pages(const mk_kv_pages& p, bool table, std::string& err) {
     if ((!p.page_table && p.table_width != 0) || misaligned4(p.page_table))
       return bad(err, "page_table is required, 4-byte aligned");
     if (p.table_width < 0 || p.table_stride < p.table_width) return bad(err, "table_stride must be >= table_width >= 0");
-    if ((long long)p.table_width * p.page_size > 0x7fffffffll)
-      return bad(err, "table_width * page_size exceeds 2^31 - 1 positions");
+    if ((long long)p.table_width * p.page_size > kMaxKeys) return bad(err, "table_width * page_size exceeds 2^31 - 1024 positions");
+  } else if (p.page_size > kMaxKeys) {
+    return bad(err, "more than 2^31 - 1024 key rows");
   }
   return MK_OK;
 }
@@ -72,6 +75,10 @@ mk_status check_append(const mk_append_args& a, std::string& err) {
     return bad(err, "batch, n_tokens or n_q_heads out of range");
   mk_status s = check_pages(a.pages, true, err);
   if (s != MK_OK) return s;
+  const mk_kv_pages& g = a.pages;
+  if ((g.page_size > 1 && g.row_stride < g.head_dim) || (g.n_kv_heads > 1 && g.head_stride < g.head_dim) ||
+      (g.n_pages > 1 && g.page_stride < g.head_dim))
+    return bad(err, "pages: rows that are written must not overlap");
   if (a.n_q_heads && !a.q) return bad(err, "n_q_heads without q");
   if (a.q) {
     if (a.n_q_heads < 1) return bad(err, "q without n_q_heads");
@@ -151,7 +158,8 @@ mk_status check_paged(const mk_paged_attn_args& a, std::string& err) {
 }
 
 mk_status check_logits(const mk_logits_args& a, std::string& err) {
-  if (a.rows < 0 || a.rows > 65535 || a.vocab < 1) return bad(err, "rows must be in [0, 65535], vocab at least 1");
+  if (a.rows < 0 || a.rows > 65535 || a.vocab < 1 || a.vocab > (1 << 30))
+    return bad(err, "rows must be in [0, 65535], vocab in [1, 2^30]");
   if (a.dtype != MK_DTYPE_FP32 && a.dtype != MK_DTYPE_BF16 && a.dtype != MK_DTYPE_FP16) return bad(err, "unknown dtype");
   const int es = a.dtype == MK_DTYPE_FP32 ? 4 : 2;
   if (!a.logits || (reinterpret_cast<uintptr_t>(a.logits) & (es - 1))) return bad(err, "logits is required, aligned to its type");

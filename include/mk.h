@@ -428,7 +428,8 @@ void mk_plan_destroy(mk_plan* p);
  *
  * For all four:
  *  - every array is device memory of the current device; arrays named const
- *    are not written;
+ *    are not written, and what is written must not overlap another argument
+ *    unless its comment says so;
  *  - the call is one or two kernel launches on `stream`, asynchronous, with no
  *    allocation, no synchronisation and no state kept from call to call; it
  *    may be captured into a CUDA graph;
@@ -459,7 +460,7 @@ typedef struct mk_kv_pages {
   void* v;
   int dtype;              /* MK_DTYPE_BF16 or MK_DTYPE_FP16 */
   int n_kv_heads, head_dim; /* head_dim 64 or 128 */
-  int n_pages, page_size; /* page_size >= 1 */
+  int n_pages, page_size; /* page_size >= 1; table_width * page_size at most 2^31 - 1024 */
   long long page_stride, head_stride, row_stride;
   const int* page_table;  /* int32 [batch][table_stride]; entries past a sequence's last page are not read */
   int table_width;        /* pages a row of the table can name */
@@ -554,7 +555,7 @@ typedef struct mk_paged_attn_args {
  * [0, vocab) in the history and the bias list are skipped.  Any of the arrays
  * below may be NULL (no such step); out and next_tokens not both. */
 typedef struct mk_logits_args {
-  int rows, vocab;
+  int rows, vocab;        /* at most 65535 and 2^30 */
   int dtype;              /* of logits: MK_DTYPE_FP32, BF16 or FP16 */
   const void* logits;     /* [rows][logits_stride] */
   long long logits_stride;

@@ -675,6 +675,53 @@ def test_captured_and_replayed_on_another_stream():
     assert torch.equal(got[0], want[1][3])
 
 
+def test_cut_prompts_captured_and_on_two_streams():
+    """Calls that join pieces: captured, replayed on new contents, and two at a time on two streams."""
+    g = gen(41)
+    x = [dev(torch.randn((2600, 4, 64), generator=g).to(BF)) for _ in range(3)]
+    q = [dev(torch.randn((30, 4, 64), generator=g).to(BF)) for _ in range(3)]
+    bounds, keys = cu([30]).to(DEV), cu([2600]).to(DEV)
+
+    def call(i, **kw):
+        return mk.prompt_attention(q[i], x[i][:, :2], x[i][:, 2:], bounds, cu_k=keys, **kw)
+
+    want = [call(i).clone() for i in range(3)]
+    qs, xs = q[0].clone(), x[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mk.prompt_attention(qs, xs[:, :2], xs[:, 2:], bounds, cu_k=keys)
+        out2 = mk.prompt_attention(qs, xs[:, :2], xs[:, 2:], bounds, cu_k=keys)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in (1, 2, 0):
+        qs.copy_(q[i])
+        xs.copy_(x[i])
+        torch.cuda.synchronize()
+        graph.replay()
+        side = [call(j, stream=s) for j, s in ((1, streams[0]), (2, streams[1]), (0, streams[0]), (1, streams[1]))]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i]) and torch.equal(out2, want[i])
+        for got, j in zip(side, (1, 2, 0, 1)):
+            assert torch.equal(got, want[j])
+
+
+def test_heads_that_share_their_rows():
+    """Pools and rows with a head stride of zero (one head's rows shown as four)."""
+    g = gen(42)
+    k, v, table = pool(g, [70, 33], 16, 1, 64, BF)
+    q = torch.randn((2, 8, 64), generator=g).to(BF)
+    kd, vd = dev(k).expand(-1, 4, -1, -1), dev(v).expand(-1, 4, -1, -1)
+    out = mk.paged_attention(dev(q), kd, vd, table.to(DEV), i32([70, 33]).to(DEV))
+    parts = [oracle.attend(q[b:b + 1], oracle.rows(k, table[b], n, 16), oracle.rows(v, table[b], n, 16), [n], 0.125)
+             for b, n in enumerate([70, 33])]
+    check_attention(out, tuple(torch.cat([p[i] for p in parts]) for i in range(3)), BF, 70, 6.0, True)
+    with pytest.raises(mk.MkError):  # nothing can be written there
+        mk.append_kv(None, dev(q)[:, :4], dev(q)[:, :4], kd, vd, table.to(DEV), i32([0, 0]).to(DEV), cu([1, 1]).to(DEV))
+    with pytest.raises(mk.MkError, match="overlap"):
+        mk.paged_attention(dev(q), dev(k), dev(v), table.to(DEV), i32([70, 33]).to(DEV),
+                           out=torch.empty((2, 1, 64), dtype=BF, device=DEV).expand(-1, 8, -1))
+
+
 def test_prompt_then_decode_steps_then_choice():
     """The operators together with the decoder: a prompt goes into the decoder's slot cache layer by layer
     (projections by torch), the decode steps continue from it, and the processed logits choose the token.  The

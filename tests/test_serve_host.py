@@ -49,7 +49,8 @@ POOL = [("pages.dtype", 2, INVALID), ("pages.head_dim", 96, UNSUPPORTED), ("page
         ("pages.n_pages", -1, INVALID), ("pages.page_size", 0, INVALID), ("pages.k", 0, INVALID),
         ("pages.v", A + 8, INVALID), ("pages.row_stride", 68, INVALID), ("pages.page_stride", 4, INVALID),
         ("pages.head_stride", -64, INVALID), ("pages.row_stride", 1 << 40, INVALID), ("pages.table_stride", 2, INVALID),
-        ("pages.table_width", -1, INVALID), ("pages.table_width", 1 << 28, INVALID)]
+        ("pages.table_width", -1, INVALID), ("pages.table_width", 1 << 28, INVALID),
+        ("pages.page_size", 0x7ffffd00 // 3, INVALID)]
 
 
 def refused(call, args, path, value, status):
@@ -67,7 +68,8 @@ def refused(call, args, path, value, status):
     ("pages.page_table", 0, INVALID), ("batch", -1, INVALID), ("n_tokens", -1, INVALID), ("n_q_heads", 0, INVALID),
     ("q_out", 0, INVALID), ("q_out", A, None), ("k", 0, INVALID), ("v", A + 2, INVALID), ("k_row_stride", 65, INVALID),
     ("q", 0, INVALID), ("cu_seqlens", 0, INVALID), ("ctx_lens", A + 1, INVALID), ("rope_theta", 0.5, INVALID),
-    ("rope_theta", math.nan, INVALID), ("status", 3, INVALID)])
+    ("rope_theta", math.nan, INVALID), ("status", 3, INVALID), ("pages.row_stride", 0, INVALID),
+    ("pages.head_stride", 56, INVALID), ("pages.page_stride", 0, INVALID)])
 def test_append_refuses(path, value, status):
     a = append_args()
     if status is None:  # on top of q with other strides
@@ -102,7 +104,7 @@ def test_paged_refuses(path, value, status):
 
 
 @pytest.mark.parametrize("path,value,status", [
-    ("rows", -1, INVALID), ("rows", 65536, INVALID), ("vocab", 0, INVALID), ("dtype", 3, INVALID), ("logits", 0, INVALID),
+    ("rows", -1, INVALID), ("rows", 65536, INVALID), ("vocab", 0, INVALID), ("vocab", (1 << 30) + 1, INVALID), ("dtype", 3, INVALID), ("logits", 0, INVALID),
     ("logits", A + 2, INVALID), ("logits_stride", 99, INVALID), ("out_stride", 99, INVALID), ("out", A + 2, INVALID),
     ("history_stride", 7, INVALID), ("history_width", -1, INVALID), ("history_width", 1 << 28, INVALID),
     ("history", 0, INVALID), ("bias_ids", 0, INVALID), ("bias_count", -1, INVALID), ("mask_stride", 3, INVALID),
