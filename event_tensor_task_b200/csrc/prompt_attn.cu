@@ -85,6 +85,7 @@ struct PromptParams {
   int sms;             // SMs of the device
   float* partial;      // results of pieces, or NULL: no sequence is cut into pieces
   int slots;           // pieces that fit there
+  int out32;           // every row of out starts on 32 bytes
 };
 
 // One piece of work: a block's row tiles of one kv head against key tiles lo .. lo + max(count).
@@ -257,6 +258,11 @@ __device__ __forceinline__ void announce(uint64_t* ready, int lane) {
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(ready);
+}
+
+// 32 bytes to a 32-byte boundary: a whole sector a lane
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), MK_W8(r, 0) : "memory");
 }
 
 // One sequence: its query rows, key rows and where they lie.
@@ -444,6 +450,8 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kSoftmaxWarps) tmem_alloc(&c.tmem, S::kTmem);
+  Walk<TILES, false> walk;
+  if (warp == kSoftmaxWarps + 3) walk.begin(P);  // (its loads travel while the block is set up)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -456,8 +464,6 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kLess));
     if (warp == kSoftmaxWarps + 3) {
       // ---- items: this block's number first, then those of blocks that have not begun, taken over one at a time
-      Walk<TILES, false> walk;
-      walk.begin(P);
       const int kv_heads = a.pages.n_kv_heads;
       long long number = blockIdx.x;
       bool fine = true;
@@ -805,42 +811,50 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
         if (!fine) break;
         tc_fence_after();
       }
-      float* part = nullptr;
       if (slot >= 0) {
-        part = P.partial + (long long)slot * S::kPartial + t * (kRows * (D + 2));
-        if (row_live && slot < P.slots) {
+        // a piece's result: m and l of the rows, then O in chunks of 8 columns, [chunk][row][8], so that a warp's rows
+        // lie next to one another
+        float* part = P.partial + (long long)slot * S::kPartial + t * (kRows * (D + 2));
+        const bool there = row_live && slot < P.slots;
+        if (there) {
           part[r] = m;
           part[kRows + r] = l;
         }
-        part += 2 * kRows + r * D;
-      }
-      const float inv = limit > 0 ? 1.f / l : 0.f;
-      T* out = static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.o_row_stride + (long long)(kvh * P.group + row_head) * a.o_head_stride;
-#pragma unroll
-      for (int i = 0; i < D; i += 32) {
-        uint32_t o[32];
         if (n_here > 0) {
-          tmem_ld32(to + i, o);
-          tmem_wait_ld();
-        }
-        if (!row_live) continue;
-        if (slot >= 0) {
-          if (n_here > 0 && slot < P.slots) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(part + i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          }
-          continue;
-        }
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + i, o);
+            tmem_wait_ld();
+            if (there) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (limit > 0) {
-            w.x = Elem<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-            w.y = Elem<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            w.z = Elem<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-            w.w = Elem<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+              for (int e = 0; e < 32; e += 8) store32(part + 2 * kRows + ((i + e) / 8 * kRows + r) * 8, o + e);
+            }
           }
-          *reinterpret_cast<uint4*>(out + i + e) = w;
+        }
+      } else {
+        const float inv = limit > 0 ? 1.f / l : 0.f;
+        T* out = static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.o_row_stride + (long long)(kvh * P.group + row_head) * a.o_head_stride;
+#pragma unroll
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          if (n_here > 0) {
+            tmem_ld32(to + i, o);
+            tmem_wait_ld();
+          }
+          if (row_live) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = limit > 0 ? Elem<T>::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
+            if (P.out32) {
+              store32(out + i, w);
+              store32(out + i + 16, w + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(out + i + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            }
+          }
         }
       }
       tc_fence_before();
@@ -912,7 +926,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Promp
     for (int i0 = 0; i0 < kJoinRows * LANES; i0 += 256) {
       const int i = i0 + tid, r = i / LANES, c = i % LANES * 4;
       if (r >= rows) continue;
-      const float* p = part + 2 * kRows + (first_row + r) * D + c;
+      const float* p = part + 2 * kRows + (c / 8 * kRows + first_row + r) * 8 + c % 8;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int k = 0; k < pieces; ++k) {
@@ -998,6 +1012,7 @@ mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err)
   P.a = a;
   P.partial = nullptr;
   P.slots = 0;
+  P.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.o_row_stride % 16 == 0 && a.o_head_stride % 16 == 0;
   const mk_kv_pages& g = a.pages;
   const int D = g.head_dim;
   P.scale_log2 = (a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;

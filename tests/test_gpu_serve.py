@@ -333,6 +333,9 @@ def test_prompt_strided_rows():
     ref = prompt_reference(qw[:, ::2, 1], [k[:20], k[20:]], [v[:20], v[20:]], [20, 30], True, 0.125)
     check_attention(out, ref, BF, 30, 6.0, False)
     assert (wide[:, :, 0] == 5.0).all() and (wide[:, :, 2] == 5.0).all()
+    wide = torch.full((50, 4, 72), 5.0, dtype=BF, device=DEV)  # rows on 16 bytes, not on 32
+    again = mk.prompt_attention(dev(qw)[:, ::2, 1], dev(k), dev(v), cu([20, 30]).to(DEV), out=wide[:, :, :64])
+    assert torch.equal(again, out) and (wide[:, :, 64:] == 5.0).all()
 
 
 def test_prompt_large_scores():
