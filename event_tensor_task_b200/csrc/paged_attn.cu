@@ -22,7 +22,7 @@
 //    what rounding takes off the probabilities (value and remainder), above 8
 //    the remainders take a second MMA: the sum sees ~16 bits of p.
 // Measured (one B200, in a graph): 475 MB of keys and values in 84 us, 78 of
-// them the first kernel (6.1 TB/s); 286 MB of 32 sequences in 57 us; one
+// them the first kernel (6.1 TB/s); 286 MB of 32 sequences in 53 us; one
 // sequence of 1,025 keys, 32/8 heads, in 6.5 us.  About 8 us of a call are
 // launch, search, the first round trips and the join, whatever its size.
 #include <algorithm>
@@ -40,15 +40,19 @@ constexpr int kRows = 16;               // query heads of a tile
 constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of a wait
 constexpr int kMaxCtas = 640;           // the workspace holds two partials of each
 
-template <int D>
+// FULL: 9 to 16 heads in a tile (both halves of the MMA's rows are heads)
+template <int D, bool FULL>
 struct Shape {
   static constexpr int kPiece = kKeys * D * 2 * 2;  // bytes of a warp's keys and values
-  static constexpr int kStages = D == 64 ? 4 : 3;
-  static constexpr int kBlocksPerSm = D == 64 ? 3 : 2;
+  // D = 128: three blocks of two stages rather than two of three (32 ragged sequences 57 -> 53 us, 200 short ones
+  // 55 -> 46 us, one long cache 84 -> 85 us), where the registers allow three
+  static constexpr int kStages = D == 64 ? 4 : FULL ? 3 : 2;
+  static constexpr int kBlocksPerSm = D == 64 || !FULL ? 3 : 2;
   static constexpr int kMerge = kRows * D * 4;       // two half output tiles in fp32
   static constexpr int kSmem = kWarps * kStages * kPiece + kMerge + 1024;
-  static constexpr int kPartial = 2 * kRows + kRows * D;  // floats: m, l, O
 };
+template <int D>
+constexpr int kPartial = 2 * kRows + kRows * D;  // floats of a partial result: m, l, O
 
 struct PagedParams {
   CUtensorMap tk, tv;  // (page_size a multiple of 16)
@@ -56,7 +60,7 @@ struct PagedParams {
   float scale_log2;
   int group, tiles;    // G; tiles of 16 heads per kv head
   int n_cta;
-  float* partial;      // [n_cta][2][kPartial]
+  float* partial;      // [n_cta][2][kPartial<D>]
 };
 
 template <class T>
@@ -176,12 +180,11 @@ __device__ __forceinline__ long long row_offset(const PagedParams& P, const Walk
   return page * g.page_stride + (long long)(w.h / P.tiles) * g.head_stride + row * g.row_stride;
 }
 
-// FULL: 9 to 16 heads in the tile (both halves of the MMA's rows are heads).
 // TMA: page_size is a multiple of 16, so a warp's 16 keys lie in one page and
 // come as boxes of 64 dimensions x 16 rows; else the rows are gathered one by one.
 template <class T, int D, bool FULL, bool TMA>
-__global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel(const __grid_constant__ PagedParams P) {
-  using S = Shape<D>;
+__global__ void __launch_bounds__(kThreads, Shape<D, FULL>::kBlocksPerSm) paged_kernel(const __grid_constant__ PagedParams P) {
+  using S = Shape<D, FULL>;
   constexpr int CH = D / 8;  // 16-byte chunks of a row
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);  // (the swizzle goes by address)
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kBlocksPerSm) paged_kernel
     float* buf = merge + (warp & 1) * ROWS * W;
     const float* other = merge + ROWS * W;
     const bool whole = n_here == use.ntile;
-    float* part = P.partial + ((long long)blockIdx.x * 2 + slot) * S::kPartial;
+    float* part = P.partial + ((long long)blockIdx.x * 2 + slot) * kPartial<D>;
     T* row0 = static_cast<T*>(P.a.out) + use.b * P.a.o_row_stride + (first_head + quad) * P.a.o_head_stride;
     T* row1 = row0 + 8 * P.a.o_head_stride;
     const float i0 = 1.f / sum0, i1 = FULL ? 1.f / sum1 : 0.f;
@@ -548,7 +551,6 @@ constexpr int kJoinThreads = 128;
 
 template <class T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ PagedParams P) {
-  using S = Shape<D>;
   constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;  // threads of a part's row, 4 values each
   __shared__ int scratch[kJoinThreads + 1];
   __shared__ float4 group_o[GROUPS][LANES];
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       po[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k <= c1) {
         // a share that begins before the pair ends with its part of it
-        const float* part = P.partial + ((long long)k * 2 + (shares.begin(k) < p0 ? 1 : 0)) * S::kPartial;
+        const float* part = P.partial + ((long long)k * 2 + (shares.begin(k) < p0 ? 1 : 0)) * kPartial<D>;
         pm[e] = part[row];
         pl[e] = part[kRows + row];
         po[e] = *reinterpret_cast<const float4*>(part + 2 * kRows + row * D + 4 * c);
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 template <class T, int D, bool FULL, bool TMA>
 mk_status launch(PagedParams& P, cudaStream_t s, std::string& err) {
-  using S = Shape<D>;
+  using S = Shape<D, FULL>;
   Device dev;
   cudaError_t e = current_device(dev);
   if (e == cudaSuccess) e = allow<paged_kernel<T, D, FULL, TMA>>(dev, S::kSmem);
@@ -661,7 +663,7 @@ mk_status pick(PagedParams& P, cudaStream_t s, std::string& err) {
 }  // namespace
 
 size_t paged_workspace_bytes(int, int, int, int head_dim) {
-  return (size_t)kMaxCtas * 2 * (head_dim <= 64 ? Shape<64>::kPartial : Shape<128>::kPartial) * sizeof(float);
+  return (size_t)kMaxCtas * 2 * (head_dim <= 64 ? kPartial<64> : kPartial<128>) * sizeof(float);
 }
 
 mk_status launch_paged(const mk_paged_attn_args& a, void* stream, std::string& err) {
