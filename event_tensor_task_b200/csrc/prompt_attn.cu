@@ -50,7 +50,7 @@ namespace {
 constexpr int kRows = 128;   // rows of a tile, keys of a tile
 constexpr int kTiles64 = 1;           // row tiles of a block at D = 64
 constexpr int kParts = 2;            // halves of a P tile, handed to the MMAs one by one
-constexpr int kShares = 2, kSlots = 4 * kShares;  // (see piece_tiles_of)
+constexpr int kShares = 2;           // of the work for each resident block (see find_cut)
 constexpr int kMostPieces = 64;       // of a block's keys
 constexpr int kLeastTiles = 6;        // key tiles of a piece: a block's way in and out costs about two
 constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
@@ -82,7 +82,7 @@ struct PromptParams {
   int group, tokens;   // G; tokens of a row tile
   int span, per_span;  // keys of a page (or of all), key tiles that cover them
   int box;             // key rows of a TMA box
-  int sms;             // SMs of the device
+  int shares;          // equal shares that the call's work is cut into
   float* partial;      // results of pieces, or NULL: no sequence is cut into pieces
   int slots;           // pieces that fit there
   int out32;           // every row of out starts on 32 bytes
@@ -307,6 +307,12 @@ __device__ __forceinline__ int ragged_tile(const PromptParams& P, const Item& i,
   return n_tiles > 0 && i.m - ((j / P.per_span) * P.span + (j % P.per_span) * kRows) < kRows ? n_tiles - 1 : -1;
 }
 
+// How long rows of keys are cut: sequences whose last block sees more than
+// `above` key tiles, into pieces of about `piece`.
+struct Cut {
+  int above, piece;
+};
+
 // How a sequence's work is laid out: row blocks, key tiles, pieces.
 template <int TILES>
 struct Work {
@@ -316,11 +322,24 @@ struct Work {
     const int full = seen > 0 ? (seen - 1) / P.span : 0;
     return seen > 0 ? full * P.per_span + (seen - full * P.span + kRows - 1) / kRows : 0;
   }
-  __device__ __forceinline__ void load(const PromptParams& P, const Seq& s, int piece_tiles) {
+  __device__ __forceinline__ void load(const PromptParams& P, const Seq& s, Cut cut) {
     blocks = (s.n + TILES * P.tokens - 1) / (TILES * P.tokens);
     tiles = blocks > 0 ? cover(P, s.m) : 0;
-    pieces = P.partial && blocks > 0 && tiles > 0 ? min(kMostPieces, (tiles + piece_tiles - 1) / piece_tiles) : 1;
+    pieces = blocks > 0 && tiles > cut.above ? min(kMostPieces, (tiles + cut.piece - 1) / cut.piece) : 1;
   }
+  // key tiles that the row tiles of a block see, and in how many pieces: a block that sees no more than one piece's is
+  // the business of its first
+  __device__ __forceinline__ int seen(const PromptParams& P, const Seq& s, int block, int (&each)[2]) const {
+    int most = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int first = (block * TILES + t) * P.tokens, last = min(s.n, first + P.tokens) - 1;
+      each[t] = t < TILES && last >= first ? cover(P, s.limit(P, last)) : 0;
+      most = max(most, each[t]);
+    }
+    return most;
+  }
+  __device__ __forceinline__ int pieces_of(int most, Cut cut) const { return most > cut.piece ? pieces : 1; }
   // the key tiles of all its blocks, as the mean of the first and the last
   __device__ __forceinline__ long long total(const PromptParams& P, const Seq& s) const {
     if (blocks == 0) return 0;
@@ -329,33 +348,44 @@ struct Work {
   }
 };
 
-// Key tiles of a piece: the whole call's work in kShares shares for each SM, not
-// below kLeastTiles.  A sequence whose blocks see more is cut into pieces of
-// that length; then no more than 4 kShares sms of them carry results to be
-// joined (blocks * tiles <= 2 total, and pieces < 2 tiles / piece_tiles where
-// there are two or more).  Found by one warp, alike wherever it is asked for.
+// The whole call's work in kShares shares for each block that the device holds
+// gives the key tiles of a piece, not below kLeastTiles.  Sequences that see
+// more are cut, but only where one sees more than twice a resident block's
+// share: its blocks would be the last to end, while cutting what evens out by
+// itself costs more than it gives (2,000 tokens, 24 heads of 64: 57 us cut, 42
+// whole).  No more than 4 times the shares carry results to be joined (blocks *
+// tiles <= 2 total, and pieces < 2 tiles / piece where there are two or more).
+// Found by one warp, alike wherever it is asked for.
 template <int TILES>
-__device__ int piece_tiles_of(const PromptParams& P) {
-  if (!P.partial) return 0x7fffffff;
+__device__ Cut find_cut(const PromptParams& P) {
+  if (!P.partial) return {0x7fffffff, 0};  // (nothing is cut, all sequences are walked at once)
   long long sum = 0;
+  int most = 0;
   for (int b = threadIdx.x & 31; b < P.a.batch; b += 32) {
     Seq s;
     s.load(P, b);
     Work<TILES> w;
-    w.load(P, s, 1);
+    w.load(P, s, {0x7fffffff, 0});
     sum += w.total(P, s);
+    most = max(most, w.tiles);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  return (int)max((long long)kLeastTiles, (sum + kShares * P.sms - 1) / (kShares * P.sms));
+  most = __reduce_max_sync(~0u, most);
+  const long long share = (sum + P.shares - 1) / P.shares;
+  const int piece = (int)min(0x7fffffffll, max((long long)kLeastTiles, share));
+  return {most >= 2 * kLeastTiles && most > 2 * kShares * share ? piece : 0x7fffffff, piece};
 }
 
 // A warp walks the sequences, 32 at a time, for the one that item or joined
 // block number `want` falls into; numbers mostly ascend, and it goes on from
-// where it was.
+// where it was.  Sequences of more key tiles than a piece's come first, so that
+// the last work to begin is short.
 template <int TILES, bool JOIN>
 struct Walk {
-  int b0 = 0, piece_tiles;
+  int b0 = 0;
+  bool second = false;  // the walk over the shorter sequences
+  Cut cut;
   long long base = 0, slot_base = 0;  // items, and results of pieces, of the sequences before b0
   long long before, count, slots, slot_before;
   Seq s;
@@ -367,8 +397,8 @@ struct Walk {
     w.pieces = 1;
     if (b < P.a.batch) {
       s.load(P, b);
-      w.load(P, s, piece_tiles);
-      const long long rows = (long long)w.blocks * P.a.pages.n_kv_heads;
+      w.load(P, s, cut);
+      const long long rows = (w.tiles > cut.piece) == second ? 0 : (long long)w.blocks * P.a.pages.n_kv_heads;
       slots = w.pieces > 1 ? rows * w.pieces : 0;
       count = JOIN ? (w.pieces > 1 ? rows : 0) : rows * w.pieces;
     }
@@ -386,7 +416,7 @@ struct Walk {
     slot_before -= slots;
   }
   __device__ __forceinline__ void begin(const PromptParams& P) {
-    piece_tiles = piece_tiles_of<TILES>(P);
+    cut = find_cut<TILES>(P);
     fill(P);
   }
   // the lane whose sequence holds `want`, or -1
@@ -394,15 +424,18 @@ struct Walk {
     if (want < base) {
       base = slot_base = 0;
       b0 = 0;
+      second = false;
       fill(P);
     }
     for (;;) {
       const unsigned hit = __ballot_sync(~0u, want >= base + before && want < base + before + count);
       if (hit) return __ffs(hit) - 1;
-      if (b0 + 32 >= P.a.batch) return -1;
+      const bool at_end = b0 + 32 >= P.a.batch;
+      if (at_end && second) return -1;
       base += __shfl_sync(~0u, before + count, 31);
       slot_base += __shfl_sync(~0u, slot_before + slots, 31);
-      b0 += 32;
+      b0 = at_end ? 0 : b0 + 32;
+      second = second || at_end;
       fill(P);
     }
   }
@@ -472,20 +505,18 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
         const int at = walk.find(P, number);
         if (at >= 0) {
           Item& it = c.item[k & 1];
+          int idle = 0;
           if (lane == at) {
             const Seq& s = walk.s;
-            const int pieces = walk.w.pieces, r = (int)(number - walk.base - walk.before);
-            const int block = walk.w.blocks - 1 - r / (kv_heads * pieces);  // a sequence's last rows see the most keys: first
-            const int kvh = r % kv_heads, piece = r / kv_heads % pieces;
-            it.first = block * TILES * P.tokens;
-            int tiles[2] = {0, 0};
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-              const int last = min(s.n, it.first + (t + 1) * P.tokens) - 1;
-              if (last >= it.first + t * P.tokens) tiles[t] = Work<TILES>::cover(P, s.limit(P, last));
-            }
-            const int n = max(tiles[0], tiles[1]), lo = (int)((long long)n * piece / pieces), hi = (int)((long long)n * (piece + 1) / pieces);
+            const int numbered = walk.w.pieces, r = (int)(number - walk.base - walk.before);
+            const int block = walk.w.blocks - 1 - r / (kv_heads * numbered);  // a sequence's last rows see the most keys: first
+            const int kvh = r % kv_heads, piece = r / kv_heads % numbered;
+            int tiles[2];
+            const int n = walk.w.seen(P, s, block, tiles), pieces = walk.w.pieces_of(n, walk.cut);
+            idle = piece >= pieces;
+            const int lo = (int)((long long)n * piece / pieces), hi = (int)((long long)n * (piece + 1) / pieces);
             it.live = 1;
+            it.first = block * TILES * P.tokens;
             it.seq = walk.b0 + lane;
             it.kvh = kvh;
             it.q0 = s.q0;
@@ -496,13 +527,14 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
 #pragma unroll
             for (int t = 0; t < 2; ++t) it.count[t] = max(0, min(tiles[t], hi) - lo);
             it.slot = -1;
-            if (pieces > 1) it.slot = (int)(walk.slot_base + walk.slot_before) + (block * kv_heads + kvh) * pieces + piece;
+            if (pieces > 1) it.slot = (int)(walk.slot_base + walk.slot_before) + (block * kv_heads + kvh) * numbered + piece;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c.item_full[k & 1]);
-          fine = await(c, &c.item_empty[k & 1], (k >> 1) & 1, a.status);  // all roles have it; the other slot is free
-          if (!fine) break;
-          ++k;
+          if (!__any_sync(~0u, idle)) {
+            if (lane == 0) mbar_arrive(&c.item_full[k & 1]);
+            fine = await(c, &c.item_empty[k & 1], (k >> 1) & 1, a.status);  // all roles have it; the other slot is free
+            if (!fine) break;
+            ++k;
+          }
         }
         uint32_t taken = 0, id = 0;
         if (lane == 0) {
@@ -869,16 +901,14 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
 }
 
 // The pieces of a (row block, kv head) joined, 32 rows of one of its row tiles
-// at a time; launched while the first kernel runs.  The pieces' weights for
-// the rows are taken first, so that no output load waits for another.
+// at a time; launched while the first kernel runs.
 constexpr int kJoinRows = 32;
 
 template <class T, int D, int TILES>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PromptParams P) {
+__global__ void __launch_bounds__(256, 4) join_kernel(const __grid_constant__ PromptParams P) {
   using S = Shape<D, TILES>;
   constexpr int LANES = D / 4, PARTS = kRows / kJoinRows;  // a thread holds 4 values of a row
   __shared__ int at[6];
-  __shared__ float weight[kMostPieces][kJoinRows];
   const mk_prompt_args& a = P.a;
   const int tid = threadIdx.x;
   Walk<TILES, true> walk;
@@ -891,67 +921,83 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Promp
       __syncwarp();
       if (tid == hit) {
         const int r = (int)(number / (PARTS * TILES) - walk.base - walk.before), kv_heads = a.pages.n_kv_heads;
+        int tiles[2];
+        const int n = walk.w.seen(P, walk.s, r / kv_heads, tiles);
         at[1] = (int)(walk.slot_base + walk.slot_before) + r * walk.w.pieces;  // (r = block * kv_heads + head)
         at[2] = r / kv_heads * TILES * P.tokens + t * P.tokens;
         at[3] = r % kv_heads;
         at[4] = walk.s.q0;
         at[5] = walk.s.n;
-        at[0] = walk.w.pieces;
+        at[0] = walk.w.pieces_of(n, walk.cut);
       }
     }
     __syncthreads();
     if (number == blockIdx.x) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pieces = at[0], slot = at[1];
     if (pieces == 0 || slot + pieces > P.slots) return;
+    if (pieces == 1) {  // (its first piece wrote the output)
+      __syncthreads();
+      continue;
+    }
     const int rows = min(kJoinRows, min(P.tokens, at[5] - at[2]) * P.group - first_row);  // (rows of tokens that exist)
     const float* part = P.partial + (long long)slot * S::kPartial + t * (kRows * (D + 2));
-    // a row's weights are 2^(m_k - m) / sum_k l_k 2^(m_k - m); a piece in which the row sees no key (m_k = -inf) has
-    // weight 0 and is not read: its output may not be there
-    if (tid < rows) {
-      const float* p = part + first_row + tid;
+    // a thread keeps a row's running maximum, sum and 4 output values, over four pieces at a time so that their loads
+    // travel together; a piece in which the row sees no key (m = -inf) counts nothing: its output may not be there
+    const int c = tid % LANES * 4;
+#pragma unroll 1
+    for (int row = first_row + tid / LANES; row < first_row + rows; row += 256 / LANES) {
       float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < pieces; ++k) m = fmaxf(m, p[(long long)k * S::kPartial]);
-#pragma unroll 4
-      for (int k = 0; k < pieces; ++k) {
-        const float w = m == -INFINITY ? 0.f : ex2(p[(long long)k * S::kPartial] - m);
-        weight[k][tid] = w;
-        l += w * p[(long long)k * S::kPartial + kRows];
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < pieces; k0 += 4) {
+        float pm[4], pl[4];
+        float4 po[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float* p = part + (long long)min(k0 + e, pieces - 1) * S::kPartial;
+          pm[e] = k0 + e < pieces ? p[row] : -INFINITY;
+          pl[e] = p[kRows + row];
+          po[e] = *reinterpret_cast<const float4*>(p + 2 * kRows + (c / 8 * kRows + row) * 8 + c % 8);
+        }
+        const float up = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
+        if (up == -INFINITY) continue;
+        const float f = ex2(m - up);
+        m = up;
+        l *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (pm[e] == -INFINITY) continue;
+          const float w = ex2(pm[e] - up);
+          l += w * pl[e];
+          o.x += w * po[e].x, o.y += w * po[e].y, o.z += w * po[e].z, o.w += w * po[e].w;
+        }
       }
       const float inv = m == -INFINITY ? 0.f : 1.f / l;
-      for (int k = 0; k < pieces; ++k) weight[k][tid] *= inv;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i0 = 0; i0 < kJoinRows * LANES; i0 += 256) {
-      const int i = i0 + tid, r = i / LANES, c = i % LANES * 4;
-      if (r >= rows) continue;
-      const float* p = part + 2 * kRows + (c / 8 * kRows + first_row + r) * 8 + c % 8;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int k = 0; k < pieces; ++k) {
-        const float w = weight[k][r];
-        if (w == 0.f) continue;
-        const float4 v = *reinterpret_cast<const float4*>(p + (long long)k * S::kPartial);
-        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
-      }
-      const int row = first_row + r;
       T* out = static_cast<T*>(a.out) + (long long)(at[4] + at[2] + row / P.group) * a.o_row_stride +
                (long long)(at[3] * P.group + row % P.group) * a.o_head_stride + c;
-      *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
+      *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
     }
-    __syncthreads();  // (at and the weights are done with)
+    __syncthreads();  // (at is done with)
   }
 }
 
 // Whether a call may cut sequences into pieces: its row blocks could leave SMs
-// idle, and there may be keys enough.
-bool may_cut(long long items, long long keys, int sms) { return items < 2ll * sms && keys >= 2ll * kLeastTiles * kRows; }
+// idle at the end, and there may be keys enough.  With more than two blocks for
+// each that the device holds the ends even out, and what looking and the second
+// launch cost is saved (3 us; 5 of 190 on 6,000 tokens, 24 heads of 64).
+bool may_cut(long long items, long long keys, int resident) { return items < 2ll * resident && keys >= 2ll * kLeastTiles * kRows; }
 
 template <int D, int TILES>
 long long items_of(const mk_prompt_args& a) {
   const int tokens = kRows / (a.n_q_heads / a.pages.n_kv_heads);
   return ((long long)a.n_tokens / (TILES * tokens) + a.batch) * a.pages.n_kv_heads;
+}
+
+template <int D, int TILES>
+size_t bytes_of(const mk_prompt_args& a, long long max_keys, int sms) {
+  using S = Shape<D, TILES>;
+  const int resident = sms * S::kBlocksPerSm;
+  return may_cut(items_of<D, TILES>(a), max_keys, resident) ? (size_t)4 * kShares * resident * S::kPartial * sizeof(float) : 0;
 }
 
 template <class T, int D, int TILES>
@@ -962,14 +1008,15 @@ mk_status launch(PromptParams& P, cudaStream_t s, std::string& err) {
   if (e == cudaSuccess) e = allow<prompt_kernel<T, D, TILES>>(dev, S::kSmem);
   if (e != cudaSuccess) return cuda_result(e, "mk_prompt_attention attributes", err);
   const mk_kv_pages& g = P.a.pages;
-  P.sms = dev.sms;
+  const int resident = dev.sms * S::kBlocksPerSm;
+  P.shares = kShares * resident;
   long long items = items_of<D, TILES>(P.a);
   const long long keys = g.page_table ? (long long)g.table_width * g.page_size : g.page_size;
-  const long long slots = std::min<long long>(kSlots * dev.sms, P.a.workspace_bytes / (S::kPartial * sizeof(float)));
-  if (P.a.workspace && slots >= kSlots * dev.sms && may_cut(items, keys, dev.sms)) {
+  const long long slots = 4ll * P.shares;
+  if (P.a.workspace && P.a.workspace_bytes >= slots * S::kPartial * sizeof(float) && may_cut(items, keys, resident)) {
     P.partial = static_cast<float*>(P.a.workspace);
     P.slots = (int)slots;
-    items += 2 * kShares * dev.sms;  // pieces: at most tiles / piece_tiles + 1 each, blocks * tiles <= 2 total
+    items += 2 * P.shares;  // pieces: at most tiles / piece_tiles + 1 each, blocks * tiles <= 2 total
   }
   if (items > 0x7fffffffll) {
     err = "too many row tiles for one launch";
@@ -1002,9 +1049,8 @@ size_t prompt_workspace_bytes(int batch, int n_tokens, int n_q_heads, int n_kv_h
   a.n_tokens = n_tokens;
   a.n_q_heads = n_q_heads;
   a.pages.n_kv_heads = n_kv_heads;
-  const bool small = head_dim <= 64;
-  if (!may_cut(small ? items_of<64, kTiles64>(a) : items_of<128, 2>(a), max_keys, dev.sms)) return 0;
-  return (size_t)kSlots * dev.sms * (small ? Shape<64, kTiles64>::kPartial : Shape<128, 2>::kPartial) * sizeof(float);
+  if (head_dim <= 64) return bytes_of<64, kTiles64>(a, max_keys, dev.sms);
+  return bytes_of<128, 2>(a, max_keys, dev.sms);
 }
 
 mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err) {
