@@ -21,9 +21,9 @@
 //    tensor pipe is nearly idle either way.  With G <= 8 the spare rows carry
 //    what rounding takes off the probabilities (value and remainder), above 8
 //    the remainders take a second MMA: the sum sees ~16 bits of p.
-// Measured (one B200, in a graph): 475 MB of keys and values in 84 us, 78 of
-// them the first kernel (6.1 TB/s); 286 MB of 32 sequences in 53 us; one
-// sequence of 1,025 keys, 32/8 heads, in 6.5 us.  About 8 us of a call are
+// Measured (one B200, in a graph): 475 MB of keys and values in 86 us, 78 of
+// them the first kernel (6.1 TB/s); 286 MB of 32 sequences in 54 us; one
+// sequence of 1,025 keys, 32/8 heads, in 6.6 us.  About 8 us of a call are
 // launch, search, the first round trips and the join, whatever its size.
 #include <algorithm>
 #include <cmath>
@@ -60,6 +60,7 @@ struct PagedParams {
   float scale_log2;
   int group, tiles;    // G; tiles of 16 heads per kv head
   int n_cta;
+  int by_pair;         // how the join's blocks are laid out
   float* partial;      // [n_cta][2][kPartial<D>]
 };
 
@@ -170,6 +171,29 @@ struct Walk {
   }
 };
 
+// The place of unit `u` (below the total), by a block of NT threads' sums in `scratch` (scan_units).
+template <int NT>
+__device__ __forceinline__ Walk walk_to(const PagedParams& P, const int* scratch, int per, int u) {
+  // the last group of sequences that begins at or before u
+  int lo = 0, hi = NT - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (scratch[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  int at = scratch[lo];
+  const int pairs = P.a.pages.n_kv_heads * P.tiles;
+  Walk w;
+  w.enter(P, lo * per);
+  while (at + w.ntile * pairs <= u) {
+    at += w.ntile * pairs;
+    w.enter(P, w.b + 1);
+  }
+  w.h = (u - at) / w.ntile;
+  w.tile = (u - at) % w.ntile;
+  return w;
+}
+
 // first element of key `t` of the pair's rows; -1: no such key (zeros)
 __device__ __forceinline__ long long row_offset(const PagedParams& P, const Walk& w, int t) {
   if (t >= w.len) return -1;
@@ -205,27 +229,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, FULL>::kBlocksPerSm) paged_
   const int total = scan_units<kThreads>(P, scratch, per);
   const Shares shares(total, P.n_cta);
   const int u0 = shares.begin(blockIdx.x), u1 = shares.begin(blockIdx.x + 1);
-  if (u0 >= u1) return;
-
-  Walk load;
-  {
-    // the last group of sequences that begins at or before u0 (all threads alike)
-    int lo = 0, hi = kThreads - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (scratch[mid] <= u0) lo = mid;
-      else hi = mid - 1;
+  // sequences without keys have zero rows; each block sees to some of them, after its share
+  auto clear_empty = [&]() {
+    for (int b = blockIdx.x; b < P.a.batch; b += gridDim.x) {
+      if (keys_of(P.a, b) > 0) continue;
+      for (int i = tid; i < P.a.n_q_heads * D; i += kThreads)
+        static_cast<T*>(P.a.out)[b * P.a.o_row_stride + i / D * P.a.o_head_stride + i % D] = static_cast<T>(0.f);
     }
-    int at = scratch[lo];
-    const int pairs = P.a.pages.n_kv_heads * P.tiles;
-    load.enter(P, lo * per);
-    while (at + load.ntile * pairs <= u0) {
-      at += load.ntile * pairs;
-      load.enter(P, load.b + 1);
-    }
-    load.h = (u0 - at) / load.ntile;
-    load.tile = (u0 - at) % load.ntile;
+  };
+  if (u0 >= u1) {
+    clear_empty();
+    return;
   }
+
+  Walk load = walk_to<kThreads>(P, scratch, per, u0);
   Walk use = load;
   const int n_units = u1 - u0;
 
@@ -540,13 +557,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, FULL>::kBlocksPerSm) paged_
     // on to the next pair (warps 1 to 3 may run ahead: the merge buffers are written again only behind a barrier)
     use.tile += n_here - 1;
     use.next(P);
-  }
+  }  clear_empty();
 }
 
-// The parts of one (sequence, query head) joined.  Launched while the first
-// kernel runs (programmatic dependent launch): it finds its place among the
-// shares, then waits for the parts.  A thread takes every GROUPS-th part, four
-// at a time so that their loads travel together, and keeps a running maximum.
+// The parts of one (sequence, query head) joined.  A block for each of them, as
+// long as these are few (by_pair); else a block for each row of the pair that a
+// share's end cuts, which works if that is the pair's first cut (4,000
+// sequences of 200 keys: 2.26 -> 0.43 ms; 32 sequences: 53 -> 55 us, so the few
+// keep the first way).  Launched while the first kernel runs (programmatic
+// dependent launch): it finds its place, then waits for the parts.  A thread
+// takes every GROUPS-th part, four at a time so that their loads travel
+// together, and keeps a running maximum.
 constexpr int kJoinThreads = 128;
 
 template <class T, int D>
@@ -555,25 +576,41 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __shared__ int scratch[kJoinThreads + 1];
   __shared__ float4 group_o[GROUPS][LANES];
   __shared__ float group_m[GROUPS], group_l[GROUPS];
-  const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   int per;
   const int total = scan_units<kJoinThreads>(P, scratch, per);
-  T* out = static_cast<T*>(P.a.out) + b * P.a.o_row_stride + head * P.a.o_head_stride;
-  const int ntile = (keys_of(P.a, b) + kUnit - 1) / kUnit;
-  const int pairs = P.a.pages.n_kv_heads * P.tiles;
-  int at = scratch[b / per];
-  for (int i = b / per * per; i < b; ++i) at += (keys_of(P.a, i) + kUnit - 1) / kUnit * pairs;
-  const int in_group = head % P.group, row = in_group % kRows;
-  const int p0 = at + ((head / P.group) * P.tiles + in_group / kRows) * ntile;
   const Shares shares(total, P.n_cta);
-  const int c0 = ntile ? shares.of(p0) : 0, c1 = ntile ? shares.of(p0 + ntile - 1) : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (ntile == 0) {
-    if (tid < D) out[tid] = static_cast<T>(0.f);
-    return;
+  const int pairs = P.a.pages.n_kv_heads * P.tiles;
+  int b = 0, head = 0, row = 0, p0 = 0, c0 = 0, c1 = 0;  // the pair's first unit, its first and last share
+  if (P.by_pair) {
+    b = blockIdx.y;
+    head = blockIdx.x;
+    const int ntile = (keys_of(P.a, b) + kUnit - 1) / kUnit, in_group = head % P.group;
+    int at = scratch[b / per];
+    for (int i = b / per * per; i < b; ++i) at += (keys_of(P.a, i) + kUnit - 1) / kUnit * pairs;
+    row = in_group % kRows;
+    p0 = at + ((head / P.group) * P.tiles + in_group / kRows) * ntile;
+    if (ntile > 0) {
+      c0 = shares.of(p0);
+      c1 = shares.of(p0 + ntile - 1);
+    }
+  } else {
+    const int cut = shares.begin(blockIdx.y + 1);
+    if (cut < total) {
+      const Walk w = walk_to<kJoinThreads>(P, scratch, per, cut);
+      row = blockIdx.x;
+      b = w.b;
+      head = (w.h / P.tiles) * P.group + (w.h % P.tiles) * kRows + row;
+      p0 = cut - w.tile;
+      c0 = blockIdx.y;
+      // (not cut, or not here first, or no such head: nothing to do)
+      c1 = w.tile > 0 && shares.begin(c0) <= p0 && row < P.group - (w.h % P.tiles) * kRows ? shares.of(p0 + w.ntile - 1) : c0;
+    }
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;  // one block had it all and wrote it
   const int g = tid / LANES, c = tid % LANES;
+  T* out = static_cast<T*>(P.a.out) + b * P.a.o_row_stride + head * P.a.o_head_stride;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = c0 + g; k0 <= c1; k0 += 4 * GROUPS) {
@@ -637,11 +674,12 @@ mk_status launch(PagedParams& P, cudaStream_t s, std::string& err) {
   if (e == cudaSuccess) e = allow<paged_kernel<T, D, FULL, TMA>>(dev, S::kSmem);
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention attributes", err);
   P.n_cta = std::min(kMaxCtas, dev.sms * S::kBlocksPerSm);
+  P.by_pair = (long long)P.a.batch * P.a.n_q_heads <= 2048;
   paged_kernel<T, D, FULL, TMA><<<P.n_cta, kThreads, S::kSmem, s>>>(P);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention launch", err);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(P.a.n_q_heads, P.a.batch);
+  cfg.gridDim = P.by_pair ? dim3(P.a.n_q_heads, P.a.batch) : dim3(std::min(P.group, kRows), P.n_cta - 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

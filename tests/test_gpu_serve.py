@@ -414,16 +414,23 @@ def test_paged(hq, hkv, d, dtype, order, page, lens):
     check_attention(out, tuple(torch.cat([p[i] for p in parts]) for i in range(3)), dtype, max(lens), 6.0, True)
 
 
-def test_paged_many_short_sequences():
-    """More pairs than blocks: a block's share holds many of them, whole and cut."""
+@pytest.mark.parametrize("n,hq,hkv,d,dtype", [
+    (300, 4, 2, 64, BF),
+    (300, 16, 2, 64, BF),     # more rows than the join takes one by one: it goes by the cuts
+    (60, 48, 2, 128, HF),     # and two tiles of heads a kv head
+])
+def test_paged_many_short_sequences(n, hq, hkv, d, dtype):
+    """More pairs than blocks: a block's share holds many of them, whole and cut, and some sequences have no keys."""
     g = gen(11)
-    lens = [int(n) for n in torch.randint(0, 200, (300,), generator=g)]
-    k, v, table = pool(g, lens, 16, 2, 64, BF)
-    q = torch.randn((300, 4, 64), generator=g).to(BF)
-    out = mk.paged_attention(dev(q), dev(k), dev(v), table.to(DEV), i32(lens).to(DEV), scale=0.2)
-    parts = [oracle.attend(q[b:b + 1], oracle.rows(k, table[b], n, 16), oracle.rows(v, table[b], n, 16), [n], 0.2)
-             for b, n in enumerate(lens)]
-    check_attention(out, tuple(torch.cat([p[i] for p in parts]) for i in range(3)), BF, 200, 6.0, True)
+    lens = [int(m) for m in torch.randint(0, 200, (n,), generator=g)]
+    lens[3] = lens[n - 1] = 0
+    k, v, table = pool(g, lens, 16, hkv, d, dtype)
+    q = torch.randn((n, hq, d), generator=g).to(dtype)
+    out = mk.paged_attention(dev(q), dev(k), dev(v), table.to(DEV), i32(lens).to(DEV), scale=0.1,
+                             out=torch.full((n, hq, d), float("nan"), dtype=dtype, device=DEV))
+    parts = [oracle.attend(q[b:b + 1], oracle.rows(k, table[b], m, 16), oracle.rows(v, table[b], m, 16), [m], 0.1)
+             for b, m in enumerate(lens)]
+    check_attention(out, tuple(torch.cat([p[i] for p in parts]) for i in range(3)), dtype, 200, 6.0, True)
 
 
 def test_paged_long_cache_offsets_past_32_bits():
