@@ -557,7 +557,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, FULL>::kBlocksPerSm) paged_
     // on to the next pair (warps 1 to 3 may run ahead: the merge buffers are written again only behind a barrier)
     use.tile += n_here - 1;
     use.next(P);
-  }  clear_empty();
+  }  if (TMA && lost) {  // no copy is in flight when the block leaves, if that can be had
+    const unsigned long long t0 = global_ns();
+    for (int i = max(0, n_units - S::kStages); i < n_units; ++i)
+      while (!mbar_try(&landed[warp][i % S::kStages], (i / S::kStages) & 1) && global_ns() - t0 < kWaitNs) {}
+  }
+  clear_empty();
 }
 
 // The parts of one (sequence, query head) joined.  A block for each of them, as
