@@ -41,6 +41,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   __shared__ int where[TOK];               // position, or -1: row behind the last sequence
   const int t0 = blockIdx.x * TOK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  dep_wait();
+  dep_launch();
 
   // a warp per token: its sequence is the number of sequences that end at or before it
   if (warp < TOK) {
@@ -141,9 +143,10 @@ template <class T, int D>
 mk_status launch(const AppendParams& P, cudaStream_t s, std::string& err) {
   // A block's tokens share its prologue (sequence search, angles); few tokens go one to a block, so that more SMs take part.
   const int n = P.a.n_tokens;
-  if (n <= kFewTokens) append_kernel<T, D, 1><<<n, kThreads, 0, s>>>(P);
-  else append_kernel<T, D, kMaxTokens><<<(n + kMaxTokens - 1) / kMaxTokens, kThreads, 0, s>>>(P);
-  return cuda_result(cudaGetLastError(), "mk_append_kv launch", err);
+  const cudaError_t e = n <= kFewTokens
+      ? mk::launch(true, append_kernel<T, D, 1>, dim3(n), kThreads, 0, s, 0, P)
+      : mk::launch(false, append_kernel<T, D, kMaxTokens>, dim3((n + kMaxTokens - 1) / kMaxTokens), kThreads, 0, s, 0, P);
+  return cuda_result(e, "mk_append_kv launch", err);
 }
 
 }  // namespace

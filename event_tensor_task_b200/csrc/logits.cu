@@ -108,6 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1) logits_kernel(const __grid_consta
   const int block_lo = (int)min((long long)a.vocab, (long long)blockIdx.x * per_block);
   const int block_hi = (int)min((long long)a.vocab, (long long)block_lo + per_block);
 
+  dep_wait();
+  dep_launch();
   float x[kPer];
   B::load(x, src + block_lo, block_hi - block_lo);
 
@@ -305,19 +307,9 @@ mk_status launch(const mk_logits_args& a, int cluster, const Device& dev, cudaSt
   if (e != cudaSuccess) return cuda_result(e, "mk_process_logits attributes", err);
   const int per_block = ((a.vocab - 1) / cluster + 128) / 128 * 128;
   const int tile = std::min<int>(per_block, kMarkBytes / sizeof(M));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster, a.rows);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.history || a.bias_indptr ? tile * sizeof(M) : 0;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_result(cudaLaunchKernelEx(&cfg, logits_kernel<T, VEC, M>, a, per_block, tile), "mk_process_logits launch", err);
+  e = mk::launch(cluster * a.rows < dev.sms, logits_kernel<T, VEC, M>, dim3(cluster, a.rows), kThreads,
+                 a.history || a.bias_indptr ? (int)(tile * sizeof(M)) : 0, s, cluster, a, per_block, tile);
+  return cuda_result(e, "mk_process_logits launch", err);
 }
 
 // Blocks of a row (a cluster): one for each SM, as long as each has 2048 ids or more.  A cluster lies within one group

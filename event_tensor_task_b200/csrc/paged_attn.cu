@@ -220,11 +220,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, FULL>::kBlocksPerSm) paged_
   float* merge = reinterpret_cast<float*>(smem + kWarps * S::kStages * S::kPiece);
   const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kPiece;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (TMA && tid == 0) {
     prefetch_map(&P.tk);
     prefetch_map(&P.tv);
   }
+  dep_wait();
+  dep_launch();
   int per;
   const int total = scan_units<kThreads>(P, scratch, per);
   const Shares shares(total, P.n_cta);
@@ -612,7 +613,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       c1 = w.tile > 0 && shares.begin(c0) <= p0 && row < P.group - (w.h % P.tiles) * kRows ? shares.of(p0 + w.ntile - 1) : c0;
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dep_wait();
+  dep_launch();
   if (c0 == c1) return;  // one block had it all and wrote it
   const int g = tid / LANES, c = tid % LANES;
   T* out = static_cast<T*>(P.a.out) + b * P.a.o_row_stride + head * P.a.o_head_stride;
@@ -680,19 +682,13 @@ mk_status launch(PagedParams& P, cudaStream_t s, std::string& err) {
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention attributes", err);
   P.n_cta = std::min(kMaxCtas, dev.sms * S::kBlocksPerSm);
   P.by_pair = (long long)P.a.batch * P.a.n_q_heads <= 2048;
-  paged_kernel<T, D, FULL, TMA><<<P.n_cta, kThreads, S::kSmem, s>>>(P);
-  e = cudaGetLastError();
+  const long long units = ((long long)P.a.pages.table_width * P.a.pages.page_size + kUnit - 1) / kUnit * P.a.batch *
+                          P.a.pages.n_kv_heads * P.tiles;
+  e = mk::launch(units <= P.n_cta, paged_kernel<T, D, FULL, TMA>, dim3(P.n_cta), kThreads, S::kSmem, s, 0, P);
   if (e != cudaSuccess) return cuda_result(e, "mk_paged_attention launch", err);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = P.by_pair ? dim3(P.a.n_q_heads, P.a.batch) : dim3(std::min(P.group, kRows), P.n_cta - 1);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_result(cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P), "mk_paged_attention join launch", err);
+  const dim3 grid = P.by_pair ? dim3(P.a.n_q_heads, P.a.batch) : dim3(std::min(P.group, kRows), P.n_cta - 1);
+  e = mk::launch(true, join_kernel<T, D>, grid, kJoinThreads, 0, s, 0, P);
+  return cuda_result(e, "mk_paged_attention join launch", err);
 }
 template <class T, int D>
 mk_status pick(PagedParams& P, cudaStream_t s, std::string& err) {

@@ -454,7 +454,6 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
   const mk_prompt_args& a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 32) {
     prefetch_map(&P.tq);
     prefetch_map(&P.tk);
@@ -484,7 +483,11 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
   }
   if (warp == kSoftmaxWarps) tmem_alloc(&c.tmem, S::kTmem);
   Walk<TILES, false> walk;
-  if (warp == kSoftmaxWarps + 3) walk.begin(P);  // (its loads travel while the block is set up)
+  if (warp == kSoftmaxWarps + 3) {  // (every other role begins with an item that this warp hands out)
+    dep_wait();
+    dep_launch();
+    walk.begin(P);  // (its loads travel while the block is set up)
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -932,7 +935,10 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const __grid_constant__ Pr
       }
     }
     __syncthreads();
-    if (number == blockIdx.x) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (number == blockIdx.x) {
+      dep_wait();
+      dep_launch();
+    }
     const int pieces = at[0], slot = at[1];
     if (pieces == 0 || slot + pieces > P.slots) return;
     if (pieces == 1) {  // (its first piece wrote the output)
@@ -1022,19 +1028,10 @@ mk_status launch(PromptParams& P, cudaStream_t s, std::string& err) {
     err = "too many row tiles for one launch";
     return MK_ERR_UNSUPPORTED;
   }
-  prompt_kernel<T, D, TILES><<<(unsigned)items, S::kThreads, S::kSmem, s>>>(P);
-  e = cudaGetLastError();
+  e = mk::launch(items <= resident, prompt_kernel<T, D, TILES>, dim3((unsigned)items), S::kThreads, S::kSmem, s, 0, P);
   if (e != cudaSuccess || !P.partial) return cuda_result(e, "mk_prompt_attention launch", err);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4 * dev.sms);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_result(cudaLaunchKernelEx(&cfg, join_kernel<T, D, TILES>, P), "mk_prompt_attention join launch", err);
+  e = mk::launch(true, join_kernel<T, D, TILES>, dim3(4 * dev.sms), 256, 0, s, 0, P);
+  return cuda_result(e, "mk_prompt_attention join launch", err);
 }
 
 }  // namespace

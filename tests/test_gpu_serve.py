@@ -715,6 +715,60 @@ def test_cut_prompts_captured_and_on_two_streams():
             assert torch.equal(got, want[j])
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_that_feed_one_another_without_a_pause(captured):
+    """Small calls begin while the one before them still runs: forty steps in which every call reads what the one
+    before it wrote (rows, cache, lengths, tokens) come out as with a pause after each call."""
+    g = gen(43)
+    B, steps = 3, 40
+    x0 = torch.randn((B, 8, 64), generator=g).to(BF)
+    lens0 = i32([5, 200, 63])
+    pool0 = [torch.randn((60, 2, 16, 64), generator=g).to(BF) for _ in range(2)]
+    table = torch.randperm(60, generator=g)[:51].view(3, 17).to(torch.int32).to(DEV)
+    W = dev((torch.randn((256, 512), generator=g) / 16).to(BF))
+    bounds, pen = cu([1] * B).to(DEV), torch.full((B,), 1.3, device=DEV)
+
+    def walk(x, lens, k, v, hist, pause):
+        """The steps' results, from x on (x, lens, k, v, hist are written)."""
+        toks = []
+        for i in range(steps):
+            q = mk.append_kv(x[:, :4], x[:, 4:6], x[:, 6:], k, v, table, lens, bounds)
+            pause()
+            lens += 1
+            a = mk.prompt_attention(q, k, v, bounds, page_table=table, kv_lens=lens)
+            pause()
+            b = mk.paged_attention(a, k, v, table, lens)
+            pause()
+            out, best = mk.process_logits(b.reshape(B, 256), history=hist, repetition=pen)
+            pause()
+            hist[:, i] = best
+            x.copy_((out.to(BF) @ W).view(B, 8, 64))
+            toks.append(best)
+        return torch.stack(toks)
+
+    def fresh():
+        return dev(x0), lens0.to(DEV), dev(pool0[0]), dev(pool0[1]), torch.full((B, steps), -1, dtype=torch.int32, device=DEV)
+
+    slow = fresh()
+    want = walk(*slow, torch.cuda.synchronize)
+    fast = fresh()
+    if captured:
+        walk(*fresh(), lambda: None)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = walk(*fast, lambda: None)
+        for t, u in zip(fast, fresh()):
+            t.copy_(u)
+        graph.replay()
+    else:
+        got = walk(*fast, lambda: None)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for t, u in zip(fast, slow):
+        assert torch.equal(t, u)
+
+
 def test_heads_that_share_their_rows():
     """Pools and rows with a head stride of zero (one head's rows shown as four)."""
     g = gen(42)
