@@ -791,7 +791,9 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
           if (lane == 0) mbar_arrive(&c.s_read[t]);
         }
         const int sub = ((lo + j) % P.per_span) * kRows;
-        const int live = min(limit - (((lo + j) / P.per_span) * P.span + sub), P.span - sub);  // columns the row sees
+        // columns that the row sees; a row that is none (behind the last token, or the tile's remainder by G) sees all,
+        // or its warp would go through the mask at every tile
+        const int live = row_live ? min(limit - (((lo + j) / P.per_span) * P.span + sub), P.span - sub) : kRows;
         if (__any_sync(~0u, live < kRows)) {
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
