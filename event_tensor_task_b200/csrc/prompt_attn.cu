@@ -47,13 +47,13 @@
 namespace mk {
 namespace {
 
-constexpr int kRows = 128;   // rows of a tile, keys of a tile
-constexpr int kTiles64 = 1;           // row tiles of a block at D = 64
-constexpr int kParts = 2;            // halves of a P tile, handed to the MMAs one by one
-constexpr int kShares = 2;           // of the work for each resident block (see find_cut)
-constexpr int kMostPieces = 64;       // of a block's keys
-constexpr int kLeastTiles = 6;        // key tiles of a piece: a block's way in and out costs about two
-constexpr float kSlack = 8.f;  // log2 growth of the maximum that is left to the probabilities
+constexpr int kRows = 128;       // rows of a tile, keys of a tile
+constexpr int kTiles64 = 1;      // row tiles of a block at D = 64
+constexpr int kParts = 2;        // halves of a P tile, handed to the MMAs one by one
+constexpr int kShares = 2;       // of the work for each resident block (see find_cut)
+constexpr int kMostPieces = 64;  // of a block's keys
+constexpr int kLeastTiles = 6;   // key tiles of a piece: a block's way in and out costs about two
+constexpr float kSlack = 8.f;    // log2 growth of the maximum that is left to the probabilities
 constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait
 
 // TILES: row tiles of a block
@@ -70,7 +70,7 @@ struct Shape {
   static constexpr bool kApart = D == 64;
   static constexpr int kP = kApart ? TILES * (kRows + D) : 0, kPStep = kApart ? 64 : 128;  // P of tile t at column kP + kPStep t
   static constexpr int kTile = kRows * D * 2;        // bytes of 128 rows
-  static constexpr int kStages = D == 64 ? (TILES == 1 ? 5 : 8) : 4;  // ring of K and V tiles
+  static constexpr int kStages = D == 64 ? 5 : 4;            // ring of K and V tiles
   static constexpr int kPartial = TILES * kRows * (D + 2);   // floats of a piece's result: m, l, O of each row tile
   static constexpr int kSmem = (TILES + kStages) * kTile + 1024;
 };
@@ -98,7 +98,7 @@ struct Item {
 };
 
 struct Control {
-  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], s_read[2], p_full[2][kParts], pv_done[2], v_tail;
+  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], s_read[2], p_full[2][kParts], pv_done[2], v_tail;
   uint64_t item_full[2], item_empty[2], next_block;
   uint4 answer;       // of the request for the next block's number
   Item item[2];
