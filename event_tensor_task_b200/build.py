@@ -22,6 +22,7 @@ CXX = os.environ.get("CXX", "g++")
 
 SOURCES = ["csrc/megakernel.cu", "csrc/plan.cpp", "csrc/api.cpp", "csrc/serve_checks.cpp", "csrc/append_kv.cu",
            "csrc/prompt_attn.cu", "csrc/paged_attn.cu", "csrc/logits.cu"]
+TENSORS_SOURCE = "csrc/tensors.cpp"
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr",
@@ -32,10 +33,17 @@ def _newer(path, than) -> bool:
     return not os.path.exists(than) or os.path.getmtime(path) > os.path.getmtime(than)
 
 
+def _headers():
+    found = [os.path.join(HERE, "build.py")] + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    for ext in ("*.h", "*.hpp", "*.cuh"):
+        found += glob.glob(os.path.join(HERE, "csrc", ext))
+    return found
+
+
 def _stale() -> bool:
-    deps = glob.glob(os.path.join(HERE, "csrc", "*")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    deps.append(os.path.join(HERE, "build.py"))
-    return any(_newer(d, out) for out in (LIB, TENSORS) for d in deps)
+    headers = _headers()
+    return (any(_newer(d, LIB) for d in [os.path.join(HERE, s) for s in SOURCES] + headers) or
+            any(_newer(d, TENSORS) for d in [os.path.join(HERE, TENSORS_SOURCE)] + headers))
 
 
 def _tensors_command():
@@ -48,7 +56,7 @@ def _tensors_command():
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", TENSORS,
-            os.path.join(HERE, "csrc/tensors.cpp")] + ["-I" + i for i in include] + [
+            os.path.join(HERE, TENSORS_SOURCE)] + ["-I" + i for i in include] + [
                 "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
@@ -66,16 +74,14 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     if not force and not _stale():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
-    headers = [os.path.join(HERE, "build.py")] + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    for ext in ("*.h", "*.hpp", "*.cuh"):
-        headers += glob.glob(os.path.join(HERE, "csrc", ext))
+    headers = _headers()
     todo, objects = [], []
     for s in SOURCES:
         src, obj = os.path.join(HERE, s), os.path.join(OBJ, os.path.basename(s) + ".o")
         objects.append(obj)
         if force or any(_newer(d, obj) for d in [src] + headers):
             todo.append([NVCC] + FLAGS + (extra or []) + ["-c", "-o", obj, src])
-    if force or any(_newer(d, TENSORS) for d in [os.path.join(HERE, "csrc/tensors.cpp")] + headers):
+    if force or any(_newer(d, TENSORS) for d in [os.path.join(HERE, TENSORS_SOURCE)] + headers):
         todo.append(_tensors_command())
     with ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as pool:
         list(pool.map(lambda cmd: _run(cmd, verbose), todo))
