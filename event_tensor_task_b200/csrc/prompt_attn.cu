@@ -42,6 +42,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "prompt_ring.hpp"
 #include "serve.cuh"
 
 namespace mk {
@@ -98,7 +99,7 @@ struct Item {
 };
 
 struct Control {
-  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], s_read[2], p_full[2][kParts], pv_done[2], v_tail;
+  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], s_read[2], p_full[2][kParts], pv_done[2], v_tail[kTails];
   uint64_t item_full[2], item_empty[2], next_block;
   uint4 answer;       // of the request for the next block's number
   Item item[2];
@@ -294,13 +295,6 @@ struct Seq {
   }
 };
 
-// The order of an item's K and V tiles in the ring (n of each): as the MMAs
-// take them, K0 V0 K1 V1 .. where P lies over S, else K0 K1 V0 K2 V1 ..
-template <bool APART>
-__device__ __forceinline__ int ring_k(int j) { return APART ? max(0, 2 * j - 1) : 2 * j; }
-template <bool APART>
-__device__ __forceinline__ int ring_v(int j, int n) { return APART ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1; }
-
 // Which of an item's key tiles the sequence ends inside: its last one or none (-1).
 __device__ __forceinline__ int ragged_tile(const PromptParams& P, const Item& i, int n_tiles) {
   const int j = i.lo + n_tiles - 1;
@@ -463,7 +457,7 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
     c.abort = 0;
     mbar_init(&c.q_full, 1);
     mbar_init(&c.q_empty, 1);
-    mbar_init(&c.v_tail, 1);
+    for (int i = 0; i < kTails; ++i) mbar_init(&c.v_tail[i], 1);
     mbar_init(&c.next_block, 1);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&c.kv_full[i], 1);
@@ -567,7 +561,7 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
       }
     } else if (warp == kSoftmaxWarps + 1) {
       // ---- loads
-      int it = 0, loaded = 0;  // tiles of the ring so far; items with keys so far
+      int it = 0, loaded = 0, tails = 0;  // tiles of the ring, items with keys, ragged value tiles so far
       bool fine = true;
       for (int k = 0; fine; ++k) {
         fine = await(c, &c.item_full[k & 1], (k >> 1) & 1, a.status);
@@ -591,13 +585,12 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
         const int boxes = kRows / P.box, ragged = ragged_tile(P, item, n_tiles);
         const int pages = a.pages.page_table ? (item.m + a.pages.page_size - 1) / a.pages.page_size : 1;
         for (int i = 0; i < 2 * n_tiles; ++i, ++it) {
-          // (tile i of the ring order: is it V, and of which key tile)
-          const bool is_v = S::kApart ? i == 2 * n_tiles - 1 || (i > 0 && !(i & 1)) : i & 1;
-          const int stage = it % S::kStages, rel = S::kApart ? (is_v ? (i == 2 * n_tiles - 1 ? n_tiles - 1 : i / 2 - 1) : (i + 1) / 2) : i >> 1;
+          const bool is_v = ring_is_v<S::kApart>(i, n_tiles);
+          const int stage = it % S::kStages, rel = ring_tile<S::kApart>(i, n_tiles);
           const int j = item.lo + rel;
           if (it >= S::kStages) fine = await(c, &c.kv_empty[stage], (it / S::kStages - 1) & 1, a.status);
           if (!fine) break;
-          uint64_t* full = is_v && rel == ragged ? &c.v_tail : &c.kv_full[stage];
+          uint64_t* full = is_v && rel == ragged ? &c.v_tail[tail_slot(tails)] : &c.kv_full[stage];
           if (lane == 0) mbar_arrive_expect_tx(full, S::kTile);
           __syncwarp();
           if (lane < boxes) {
@@ -618,6 +611,7 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
           }
           __syncwarp();
         }
+        tails += ragged >= 0;
       }
       // no copy is in flight when the block leaves, even if another role has given up
       if (loaded > 0) drain(&c.q_full, (loaded - 1) & 1);
@@ -736,7 +730,7 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
         if (!item.live) break;
         const int n_tiles = max(item.count[0], item.count[1]), ragged = ragged_tile(P, item, n_tiles);
         if (ragged >= 0) {
-          if (!await(c, &c.v_tail, cleared & 1, a.status)) break;
+          if (!await(c, &c.v_tail[tail_slot(cleared)], tail_parity(cleared), a.status)) break;
           ++cleared;
           const int j = item.lo + ragged, stage = (it + ring_v<S::kApart>(ragged, n_tiles)) % S::kStages;
           const int live = item.m - ((j / P.per_span) * P.span + (j % P.per_span) * kRows);

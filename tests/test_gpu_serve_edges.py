@@ -1,0 +1,58 @@
+"""The serving operators at calls that the first tests do not make: short prompts in great number, pools without pages,
+calls from two threads and the like.  Tolerances as in test_gpu_serve.py."""
+import math
+
+import pytest
+import torch
+
+import event_tensor_task_b200 as mk
+from oracle import serve as oracle
+from test_gpu_serve import BF, DEV, HF, check_attention, cu, dev, gen, i32, prompt_reference, status_word
+
+pytestmark = pytest.mark.gpu
+
+
+def flush():
+    """Nothing of what was there before stays in L2 (126 MB)."""
+    torch.zeros(1 << 26, device=DEV)
+
+
+@pytest.mark.parametrize("hkv,d,dtype", [(8, 64, BF), (4, 128, HF)])
+def test_short_prompts_in_great_number(hkv, d, dtype):
+    """Every block runs dozens of pieces of work of one or two key tiles, each ending inside its last value tile, out of
+    key and value pools that are not in L2.  The rows are those of calls too small for a block to get a second piece."""
+    g = gen(hkv)
+    n, page = 1200, 64
+    lens = [int(m) for m in torch.randint(1, 129, (n,), generator=g)]
+    need = [-(-m // page) for m in lens]
+    total = 4 * sum(need)
+    where = torch.randperm(total, generator=g)[:sum(need)].to(torch.int32)
+    table = torch.full((n, 2), -1, dtype=torch.int32)
+    at = 0
+    for b, m in enumerate(need):
+        table[b, :m] = where[at:at + m]
+        at += m
+    dgen = torch.Generator(device=DEV).manual_seed(d)
+    k, v = (torch.randn((total, hkv, page, d), generator=dgen, device=DEV).to(dtype) for _ in range(2))
+    q = torch.randn((sum(lens), hkv, d), generator=dgen, device=DEV).to(dtype)
+    table, bounds = table.to(DEV), cu(lens)
+    few = 120 // hkv
+    want, st = torch.empty_like(q), status_word()
+    for b in range(0, n, few):
+        e = min(n, b + few)
+        lo, hi = int(bounds[b]), int(bounds[e])
+        want[lo:hi] = mk.prompt_attention(q[lo:hi], k, v, (bounds[b:e + 1] - lo).to(DEV), page_table=table[b:e],
+                                          kv_lens=i32(lens[b:e]).to(DEV), status=st)
+    assert int(st) == 0
+    on_device = bounds.to(DEV), i32(lens).to(DEV)
+    for _ in range(8):
+        flush()
+        out = mk.prompt_attention(q, k, v, on_device[0], page_table=table, kv_lens=on_device[1], status=st,
+                                  out=torch.full_like(q, math.nan))
+        torch.cuda.synchronize()
+        assert int(st) == 0 and torch.equal(out, want)
+    for b in range(0, n, 100):  # and the rows are right
+        lo, m = int(bounds[b]), lens[b]
+        rows = [torch.cat([pool[int(p)].transpose(0, 1) for p in table[b, :need[b]]])[:m].cpu() for pool in (k, v)]
+        ref = prompt_reference(q[lo:lo + m].cpu(), rows[:1], rows[1:], [m], True, d ** -0.5)
+        check_attention(out[lo:lo + m], ref, dtype, 128, 6.0, False)
