@@ -277,7 +277,8 @@ struct Seq {
     n = max(min(c1, a.n_tokens), q0) - q0;
     bool fine = c0 == q0 && c1 == q0 + n;
     if (a.pages.page_table) {
-      const int cap = a.pages.table_width * a.pages.page_size, l = __ldg(a.kv_lens + b);
+      // (a pool without pages holds no keys, whatever the table names: there is no tensor map of it to load by)
+      const int cap = a.pages.n_pages > 0 ? a.pages.table_width * a.pages.page_size : 0, l = __ldg(a.kv_lens + b);
       k0 = 0;
       m = min(max(l, 0), cap);
       fine = fine && l == m;
@@ -1069,7 +1070,7 @@ mk_status launch_prompt(const mk_prompt_args& a, void* stream, std::string& err)
       return MK_ERR_UNSUPPORTED;
     }
   }
-  // (no keys at all: nothing is loaded, the maps are those of q)
+  // (no keys at all: nothing is loaded, see Seq; the maps are those of q)
   P.tk = P.tv = P.tq;
   if (g.n_pages > 0 && g.page_size > 0 && !encode_pages(&P.tk, &P.tv, g, P.box)) {
     err = "the driver takes no tensor map of the keys' strides";

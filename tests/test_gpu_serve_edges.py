@@ -56,3 +56,23 @@ def test_short_prompts_in_great_number(hkv, d, dtype):
         rows = [torch.cat([pool[int(p)].transpose(0, 1) for p in table[b, :need[b]]])[:m].cpu() for pool in (k, v)]
         ref = prompt_reference(q[lo:lo + m].cpu(), rows[:1], rows[1:], [m], True, d ** -0.5)
         check_attention(out[lo:lo + m], ref, dtype, 128, 6.0, False)
+
+
+@pytest.mark.parametrize("width,keys", [(3, 5), (200, 3000)])  # (few keys; enough to be cut into pieces)
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, HF)])
+def test_a_pool_without_pages_holds_no_keys(d, dtype, width, keys):
+    """Whatever the table and the lengths say: zero rows, nothing stored, and the status word."""
+    k, v = torch.empty((2, 0, 2, 16, d), dtype=dtype, device=DEV)
+    table, q = torch.zeros((2, width), dtype=torch.int32, device=DEV), torch.ones((6, 4, d), dtype=dtype, device=DEV)
+    st = status_word()
+    out = mk.prompt_attention(q, k, v, cu([5, 1]).to(DEV), page_table=table, kv_lens=i32([keys, 0]).to(DEV), status=st)
+    torch.cuda.synchronize()
+    assert int(st) == mk.MK_ERR_DEVICE_BOUNDS and (out == 0).all()
+    st.zero_()
+    out = mk.prompt_attention(q, k, v, cu([5, 1]).to(DEV), page_table=table, kv_lens=i32([0, 0]).to(DEV), status=st)
+    assert int(st) == 0 and (out == 0).all()
+    out = mk.paged_attention(q[:2], k, v, table, i32([keys, 0]).to(DEV), status=st)
+    assert int(st) == mk.MK_ERR_DEVICE_BOUNDS and (out == 0).all()
+    st.zero_()
+    mk.append_kv(q, q[:, :2], q[:, 2:], k, v, table, i32([0, 0]).to(DEV), cu([5, 1]).to(DEV), status=st)
+    assert int(st) == mk.MK_ERR_DEVICE_BOUNDS
