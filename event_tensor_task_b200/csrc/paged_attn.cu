@@ -29,6 +29,7 @@
 #include <cmath>
 
 #include "serve.cuh"
+#include "waits.hpp"
 
 namespace mk {
 namespace {
@@ -95,6 +96,16 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// a warp that waits for a phase of an mbarrier (wait_together)
+struct Landing {
+  uint64_t* bar;
+  uint32_t parity;
+  __device__ __forceinline__ bool there() const { return mbar_try(bar, parity); }
+  __device__ __forceinline__ bool all(bool p) const { return __all_sync(~0u, p); }
+  __device__ __forceinline__ bool any(bool p) const { return __any_sync(~0u, p); }
+  __device__ __forceinline__ unsigned long long now() const { return global_ns(); }
+};
 
 // keys of sequence b that are there to see
 __device__ __forceinline__ int keys_of(const mk_paged_attn_args& a, int b) {
@@ -348,18 +359,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, FULL>::kBlocksPerSm) paged_
       issue();
       const uint32_t at = ring + (u % S::kStages) * S::kPiece;
       if (TMA) {
-        uint64_t* bar = &landed[warp][u % S::kStages];
-        const uint32_t parity = (u / S::kStages) & 1;
-        if (!lost && !mbar_try(bar, parity)) {
-          const unsigned long long t0 = global_ns();
-          while (!mbar_try(bar, parity)) {
-            if (global_ns() - t0 > kWaitNs) {
-              if (P.a.status) *P.a.status = MK_ERR_DEVICE_TIMEOUT;
-              lost = true;
-              break;
-            }
-          }
-          lost = __any_sync(~0u, lost);
+        Landing piece{&landed[warp][u % S::kStages], (uint32_t)(u / S::kStages) & 1};
+        if (!lost && !wait_together(piece, kWaitNs)) {
+          if (P.a.status) *P.a.status = MK_ERR_DEVICE_TIMEOUT;
+          lost = true;
         }
       } else {
         cp_wait<S::kStages - 1>();
@@ -558,7 +561,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, FULL>::kBlocksPerSm) paged_
     // on to the next pair (warps 1 to 3 may run ahead: the merge buffers are written again only behind a barrier)
     use.tile += n_here - 1;
     use.next(P);
-  }  if (TMA && lost) {  // no copy is in flight when the block leaves, if that can be had
+  }
+  if (TMA && lost) {  // no copy is in flight when the block leaves, if that can be had
     const unsigned long long t0 = global_ns();
     for (int i = max(0, n_units - S::kStages); i < n_units; ++i)
       while (!mbar_try(&landed[warp][i % S::kStages], (i / S::kStages) & 1) && global_ns() - t0 < kWaitNs) {}
