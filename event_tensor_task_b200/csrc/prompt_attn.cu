@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
         if (at >= 0) {
           Item& it = c.item[k & 1];
           int idle = 0;
-          if (lane == at) {
+          if (lane == at) {  // (the lane that writes the item also hands it out: its arrival is behind its writes)
             const Seq& s = walk.s;
             const int numbered = walk.w.pieces, r = (int)(number - walk.base - walk.before);
             const int block = walk.w.blocks - 1 - r / (kv_heads * numbered);  // a sequence's last rows see the most keys: first
@@ -526,9 +526,9 @@ __global__ void __launch_bounds__(Shape<D, TILES>::kThreads, Shape<D, TILES>::kB
             for (int t = 0; t < 2; ++t) it.count[t] = max(0, min(tiles[t], hi) - lo);
             it.slot = -1;
             if (pieces > 1) it.slot = (int)(walk.slot_base + walk.slot_before) + (block * kv_heads + kvh) * numbered + piece;
+            if (!idle) mbar_arrive(&c.item_full[k & 1]);
           }
           if (!__any_sync(~0u, idle)) {
-            if (lane == 0) mbar_arrive(&c.item_full[k & 1]);
             fine = await(c, &c.item_empty[k & 1], (k >> 1) & 1, a.status);  // all roles have it; the other slot is free
             if (!fine) break;
             ++k;

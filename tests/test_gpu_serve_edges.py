@@ -76,3 +76,32 @@ def test_a_pool_without_pages_holds_no_keys(d, dtype, width, keys):
     st.zero_()
     mk.append_kv(q, q[:, :2], q[:, 2:], k, v, table, i32([0, 0]).to(DEV), cu([5, 1]).to(DEV), status=st)
     assert int(st) == mk.MK_ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, HF)])
+def test_work_handed_out_by_every_lane(d, dtype):
+    """Seventy sequences, so every lane of the warp that hands out the work finds and publishes some of it; a few are
+    cut into pieces, of which the blocks that see few keys leave all but the first idle."""
+    g = gen(d)
+    new = [int(n) for n in torch.randint(1, 30, (70,), generator=g)]
+    keys = [n + int(e) for n, e in zip(new, torch.randint(0, 100, (70,), generator=g))]
+    for b in (2, 33, 69):
+        new[b], keys[b] = 140, 2600
+    keys[33] = 1700
+    new[2] = 1500  # its first rows see about a thousand keys, its last 2,600
+    q = torch.randn((sum(new), 2, d), generator=g).to(dtype)
+    kv = torch.randn((sum(keys), 2, d), generator=g).to(dtype)
+    x, st = dev(kv), status_word()
+    args = dev(q), x[:, :1], x[:, 1:], cu(new).to(DEV)
+    assert mk.mk_prompt_attention_workspace_bytes(70, sum(new), 2, 1, d, sum(keys)) > 0
+    outs = [mk.prompt_attention(*args, cu_k=cu(keys).to(DEV), status=st) for _ in range(5)]
+    whole = mk.prompt_attention(*args, cu_k=cu(keys).to(DEV), status=st, workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+    torch.cuda.synchronize()
+    assert int(st) == 0 and all(torch.equal(outs[0], o) for o in outs)
+    qb, kb = cu(new), cu(keys)
+    for b in range(70):
+        some = torch.arange(0, new[b], 97 if new[b] > 200 else 1)
+        k, v = kv[kb[b]:kb[b + 1], :1], kv[kb[b]:kb[b + 1], 1:]
+        ref = oracle.attend(q[qb[b] + some], k, v, [int(i) + 1 + keys[b] - new[b] for i in some], d ** -0.5)
+        for out in (outs[0], whole):
+            check_attention(out[int(qb[b]) + some.to(DEV)], ref, dtype, keys[b], 6.0, False)
