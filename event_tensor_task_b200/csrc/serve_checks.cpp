@@ -1,5 +1,6 @@
 // serve_checks.cpp — host checks of the serving operators' arguments
 // (include/mk.h): everything that can be told without reading device memory.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -58,6 +59,21 @@ mk_status check_pages(const mk_kv_pages& p, bool table, std::string& err) {
   return MK_OK;
 }
 
+// Whether rows of d elements along three dimensions lie on top of one another: from the smallest stride on, each must
+// reach past all that the dimensions inside it span.  (A dimension of one entry has no stride.)
+bool rows_overlap(int d, const long long (&count)[3], const long long (&stride)[3]) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int x, int y) { return stride[x] < stride[y]; });
+  long long span = d;
+  for (int i : order) {
+    if (count[i] <= 1) continue;
+    if (stride[i] < span) return true;
+    if (stride[i] > (1ll << 61) / count[i]) span = 1ll << 61;  // (longer than any stride can be)
+    else span += (count[i] - 1) * stride[i];
+  }
+  return false;
+}
+
 mk_status check_heads(int n_q, int n_kv, std::string& err) {
   if (n_q < 1 || n_q > 65535 || n_q % n_kv) return bad(err, "n_q_heads must be a multiple of n_kv_heads, at most 65535");
   return MK_OK;
@@ -76,8 +92,7 @@ mk_status check_append(const mk_append_args& a, std::string& err) {
   mk_status s = check_pages(a.pages, true, err);
   if (s != MK_OK) return s;
   const mk_kv_pages& g = a.pages;
-  if ((g.page_size > 1 && g.row_stride < g.head_dim) || (g.n_kv_heads > 1 && g.head_stride < g.head_dim) ||
-      (g.n_pages > 1 && g.page_stride < g.head_dim))
+  if (rows_overlap(g.head_dim, {g.n_pages, g.n_kv_heads, g.page_size}, {g.page_stride, g.head_stride, g.row_stride}))
     return bad(err, "pages: rows that are written must not overlap");
   if (a.n_q_heads && !a.q) return bad(err, "n_q_heads without q");
   if (a.q) {
