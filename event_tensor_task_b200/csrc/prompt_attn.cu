@@ -996,11 +996,23 @@ long long items_of(const mk_prompt_args& a) {
   return ((long long)a.n_tokens / (TILES * tokens) + a.batch) * a.pages.n_kv_heads;
 }
 
+// Results of pieces that a call can leave: by its work no more than 4 for each share (find_cut), and by its size no more
+// than a block and head can be cut into, at kLeastTiles a piece (one prompt of 17 tokens over a cache of 2,048 rows: 6
+// of them, not the 2,368 of the whole device).
+long long slots_of(long long items, long long key_tiles, int shares) {
+  const long long pieces = std::min<long long>(kMostPieces, (key_tiles + kLeastTiles - 1) / kLeastTiles);
+  return std::min(4ll * shares, items * pieces);
+}
+
+// (Pages that are no multiple of a tile take more tiles than their keys fill, less than twice as many: a page that is cut
+// holds at least one whole tile.)
 template <int D, int TILES>
 size_t bytes_of(const mk_prompt_args& a, long long max_keys, int sms) {
   using S = Shape<D, TILES>;
   const int resident = sms * S::kBlocksPerSm;
-  return may_cut(items_of<D, TILES>(a), max_keys, resident) ? (size_t)4 * kShares * resident * S::kPartial * sizeof(float) : 0;
+  const long long items = items_of<D, TILES>(a);
+  if (!may_cut(items, max_keys, resident)) return 0;
+  return slots_of(items, 2 * (max_keys / kRows) + 1, kShares * resident) * S::kPartial * sizeof(float);
 }
 
 template <class T, int D, int TILES>
@@ -1015,7 +1027,7 @@ mk_status launch(PromptParams& P, cudaStream_t s, std::string& err) {
   P.shares = kShares * resident;
   long long items = items_of<D, TILES>(P.a);
   const long long keys = g.page_table ? (long long)g.table_width * g.page_size : g.page_size;
-  const long long slots = 4ll * P.shares;
+  const long long slots = slots_of(items, keys / P.span * P.per_span + (keys % P.span + kRows - 1) / kRows, P.shares);
   if (P.a.workspace && P.a.workspace_bytes >= slots * S::kPartial * sizeof(float) && may_cut(items, keys, resident)) {
     P.partial = static_cast<float*>(P.a.workspace);
     P.slots = (int)slots;

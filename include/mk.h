@@ -514,7 +514,7 @@ typedef struct mk_prompt_args {
   const int* cu_q;        /* int32 [batch + 1]: query rows of each sequence */
   const int* cu_k;        /* int32 [batch + 1]: key rows (packed keys) */
   const int* kv_lens;     /* int32 [batch]: keys of each sequence (paged keys) */
-  void* workspace;        /* mk_prompt_attention_workspace_bytes, 256-byte aligned, or NULL: no sequence is cut
+  void* workspace;        /* mk_prompt_attention_workspace_bytes, 256-byte aligned; NULL or less: no sequence is cut
                              along its keys, so few row tiles leave SMs idle; need not be cleared, not to be
                              shared by calls that overlap on the device */
   size_t workspace_bytes;
@@ -583,7 +583,10 @@ mk_status mk_append_kv(const mk_append_args* a, void* stream);
 /* Workspace with which mk_prompt_attention cuts long rows of keys into pieces
  * that a second kernel joins; 0 where a call of this size does not (max_keys:
  * the most keys a sequence can have, table_width * page_size or the rows of
- * k).  For the current device. */
+ * k).  It goes by the row blocks and the pieces that max_keys can be cut into
+ * (one prompt of 17 tokens, 4 heads of 64, 2,048 keys: 0.4 MB) and ends where
+ * the device is full (148 SMs: 80 MB at head_dim 64, 158 MB at 128).  For the
+ * current device. */
 size_t mk_prompt_attention_workspace_bytes(int batch, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
                                            long long max_keys);
 mk_status mk_prompt_attention(const mk_prompt_args* a, void* stream);

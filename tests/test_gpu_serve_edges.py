@@ -105,3 +105,58 @@ def test_work_handed_out_by_every_lane(d, dtype):
         ref = oracle.attend(q[qb[b] + some], k, v, [int(i) + 1 + keys[b] - new[b] for i in some], d ** -0.5)
         for out in (outs[0], whole):
             check_attention(out[int(qb[b]) + some.to(DEV)], ref, dtype, keys[b], 6.0, False)
+
+
+def test_prompt_workspace_goes_by_the_call():
+    """A short prompt over the decoder's slot cache takes kilobytes, not what the whole device could leave; the most that
+    any call takes is what it was."""
+    small = mk.mk_prompt_attention_workspace_bytes(1, 17, 4, 2, 64, 2048)
+    assert 0 < small <= 1 << 20
+    k, v = torch.zeros((2, 4, 2, 2048, 64), dtype=BF, device=DEV)
+    q = torch.zeros((17, 4, 64), dtype=BF, device=DEV)
+    args = cu([17]).to(DEV), i32([[2]]).to(DEV), i32([17]).to(DEV)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    mk.prompt_attention(q, k, v, args[0], page_table=args[1], kv_lens=args[2])
+    assert torch.cuda.max_memory_allocated() - before <= 2 << 20
+    for d in (64, 128):
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        tiles = 2 * sms  # of 128 rows, that the device holds
+        whole = mk.mk_prompt_attention_workspace_bytes(1, 128 * sms, 1, 1, d, 1 << 22)
+        assert whole == 4 * 2 * tiles * 128 * (d + 2) * 4
+
+
+@pytest.mark.parametrize("page", [16, 128, 130, 255, 1024])
+@pytest.mark.parametrize("hq,hkv,d,new,lens", [
+    (4, 2, 64, [17], [2300]),
+    (2, 1, 128, [1, 9, 260], [1800, 40, 2100]),
+    (6, 2, 64, [64, 65, 1], [1700, 900, 2550]),
+])
+def test_prompt_workspace_is_enough(page, hq, hkv, d, new, lens):
+    """Nothing is written behind it, and what comes out is what comes out with one as large as any call's."""
+    g = gen(page + d)
+    k, v, table = (t.to(DEV) for t in _filled_pool(g, lens, page, hkv, d))
+    q = torch.randn((sum(new), hq, d), generator=g).to(BF).to(DEV)
+    tail = cu(new).to(DEV), i32(lens).to(DEV)
+    n = mk.mk_prompt_attention_workspace_bytes(len(new), sum(new), hq, hkv, d, page * table.shape[1])
+    assert n > 0 and n % 16 == 0
+    buf = torch.full((n + 4096,), 171, dtype=torch.uint8, device=DEV)
+    st = status_word()
+    outs = [mk.prompt_attention(q, k, v, tail[0], page_table=table, kv_lens=tail[1], workspace=w, status=st)
+            for w in (buf[:n], None, torch.empty(200 << 20, dtype=torch.uint8, device=DEV))]
+    torch.cuda.synchronize()
+    assert int(st) == 0 and (buf[n:] == 171).all() and not (buf[:n] == 171).all()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def _filled_pool(g, lens, page, hkv, d):
+    need = [-(-n // page) for n in lens]
+    perm = torch.randperm(sum(need), generator=g).to(torch.int32)
+    table, at = torch.full((len(lens), max(need)), -1, dtype=torch.int32), 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    k, v = torch.randn((2, sum(need), hkv, page, d), generator=g).to(BF)
+    return k, v, table
