@@ -142,8 +142,9 @@ float scale_of(PyObject* o) {
   if (o == Py_None) return 0.f;
   const double s = PyFloat_AsDouble(o);
   if (PyErr_Occurred()) throw python_error();
-  if (!(s > 0.0)) refuse("scale must be above 0");
-  return static_cast<float>(s);
+  const float f = static_cast<float>(s);
+  if (!(f > 0.f)) refuse("scale must be above 0 in fp32");  // (0 would stand for 1 / sqrt(head_dim))
+  return f;
 }
 
 // Where a call runs: every tensor on one CUDA device, that device current, and

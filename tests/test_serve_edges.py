@@ -2,7 +2,7 @@
 import pytest
 
 import event_tensor_task_b200 as mk
-from test_serve_host import INVALID, append_args
+from test_serve_host import INVALID, append_args, calls, tensors
 
 
 @pytest.mark.parametrize("row,head,page", [
@@ -33,3 +33,12 @@ def test_append_takes_pools_in_any_order_of_their_dimensions(row, head, page):
     a.rope_theta = 0.5  # refused for this, which is looked at after the pool
     with pytest.raises(mk.MkError, match="rope_theta"):
         mk.mk_append_kv(a)
+
+
+@pytest.mark.parametrize("name", ["prompt", "paged"])
+@pytest.mark.parametrize("scale", [1e-50, 5e-324, 0.0, float("nan")])
+def test_a_scale_that_fp32_rounds_to_zero_is_refused(name, scale):
+    """(it would become the default scale)"""
+    with pytest.raises(mk.MkError, match="scale") as e:
+        calls(tensors(), scale=scale)[name]()
+    assert e.value.status == INVALID
