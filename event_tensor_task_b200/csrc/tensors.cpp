@@ -270,6 +270,7 @@ PyObject* prompt(PyObject* const* o) {
   a.n_tokens = as_int(n, "q");
   a.n_q_heads = as_int(heads, "q");
   a.causal = PyObject_IsTrue(o[7]);
+  if (a.causal < 0) throw python_error();
   a.scale = scale_of(o[8]);
   rows("q", q, n, heads, p.head_dim, k.scalar_type(), a.q, a.q_row_stride, a.q_head_stride);
   a.cu_q = static_cast<const int*>(array("cu_q", &cu_q, at::kInt, batch + 1));

@@ -1,5 +1,6 @@
 """The serving operators' refusals at the edges, without a GPU."""
 import pytest
+import torch
 
 import event_tensor_task_b200 as mk
 from test_serve_host import INVALID, append_args, calls, tensors
@@ -42,3 +43,12 @@ def test_a_scale_that_fp32_rounds_to_zero_is_refused(name, scale):
     with pytest.raises(mk.MkError, match="scale") as e:
         calls(tensors(), scale=scale)[name]()
     assert e.value.status == INVALID
+
+
+def test_causal_without_a_truth_value_raises_its_own_error():
+    x = tensors()
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        mk.prompt_attention(x["q"], x["k"], x["k"], x["cu"], causal=torch.ones(2))
+    none = x["q"][:0]
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        mk.prompt_attention(none, none[:, :2], none[:, :2], torch.zeros(1, dtype=torch.int32), causal=torch.ones(2))
