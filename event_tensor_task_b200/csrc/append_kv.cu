@@ -69,6 +69,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       where[warp] = pos;
       dest[warp] = d;
     }
+  } else if (blockIdx.x == 0 && warp == kThreads / 32 - 1 && a.status) {
+    // meanwhile, once a call: bounds that descend or go past the rows (what they hide, no row's search can tell)
+    bool bad = false;
+    for (int b = lane; b < a.batch; b += 32) {
+      const int begin = __ldg(a.cu_seqlens + b), end = __ldg(a.cu_seqlens + b + 1);
+      bad = bad || begin < 0 || end < begin || end > a.n_tokens;
+    }
+    if (bad) report_bounds(a.status);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < TOK * H; i += kThreads) {

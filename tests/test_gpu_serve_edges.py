@@ -160,3 +160,29 @@ def _filled_pool(g, lens, page, hkv, d):
         at += n
     k, v = torch.randn((2, sum(need), hkv, page, d), generator=g).to(BF)
     return k, v, table
+
+
+@pytest.mark.parametrize("bounds,fine", [
+    ([0, 2, 6], True),
+    ([1, 2, 4], True),          # rows before the first sequence and behind the last
+    ([0, 2, 7], False),         # more rows than there are
+    ([0, 5, 3, 6], False),      # a sequence of fewer than no rows
+    ([0, 6, 6, 5], False),
+    ([0] * 299 + [6, 2], False),
+    ([-1, 2, 6], False),
+    ([0, 2, 2**31 - 1], False),
+])
+def test_append_reports_bounds_of_sequences(bounds, fine):
+    g = gen(71)
+    B = len(bounds) - 1
+    k, v = torch.zeros((2, B, 2, 16, 64), dtype=BF, device=DEV)
+    x = torch.randn((6, 2, 64), generator=g).to(BF).to(DEV)
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None]
+    st = status_word()
+    mk.append_kv(None, x, x, k, v, table, torch.zeros(B, dtype=torch.int32, device=DEV), i32(bounds).to(DEV),
+                 rope_theta=0, status=st)
+    assert int(st) == (0 if fine else mk.MK_ERR_DEVICE_BOUNDS)
+    if fine or bounds == [0, 2, 7]:  # rows that exist are stored
+        for b in range(2):
+            lo, hi = bounds[b], min(bounds[b + 1], 6)
+            assert torch.equal(v[b, :, :hi - lo], x[lo:hi].transpose(0, 1)) and (v[b, :, hi - lo:] == 0).all()
