@@ -186,3 +186,113 @@ def test_append_reports_bounds_of_sequences(bounds, fine):
         for b in range(2):
             lo, hi = bounds[b], min(bounds[b + 1], 6)
             assert torch.equal(v[b, :, :hi - lo], x[lo:hi].transpose(0, 1)) and (v[b, :, hi - lo:] == 0).all()
+
+
+def _program(seed, d=64, dtype=BF):
+    """A short serving step on tensors of its own: a function that runs it and returns all that it wrote."""
+    g = gen(seed)
+    new, ctx = [9, 1, 40], [30, 2000, 3]
+    lens = [a + c for a, c in zip(new, ctx)]
+    k, v, table = (t.to(DEV) for t in _filled_pool(g, lens, 16, 2, d))
+    x = torch.randn((sum(new), 8, d), generator=g).to(dtype).to(DEV)
+    W = (torch.randn((4 * d, 5000), generator=g) / 16).to(dtype).to(DEV)
+    ctx, lens, bounds = i32(ctx).to(DEV), i32(lens).to(DEV), cu(new).to(DEV)
+    last = (bounds[1:] - 1).long()
+    hist, pen = torch.randint(0, 5000, (3, 50), generator=g, dtype=torch.int32).to(DEV), torch.full((3,), 1.3, device=DEV)
+
+    def run(split=None):
+        kc, vc = k.clone(), v.clone()
+        q = mk.append_kv(x[:, :4], x[:, 4:6], x[:, 6:], kc, vc, table, ctx, bounds)
+        if split is None:
+            a = mk.prompt_attention(q, kc, vc, bounds, page_table=table, kv_lens=lens)
+            b = mk.paged_attention(q[last], kc, vc, table, lens)
+        else:  # the two attentions side by side
+            here = torch.cuda.current_stream()
+            split.wait_stream(here)
+            with torch.cuda.stream(split):
+                b = mk.paged_attention(q[last], kc, vc, table, lens)
+            a = mk.prompt_attention(q, kc, vc, bounds, page_table=table, kv_lens=lens)
+            here.wait_stream(split)
+        joined = (a[last] + b).reshape(3, -1)
+        out, best = mk.process_logits(joined @ W, history=hist, repetition=pen)
+        return [kc, vc, q, a, b, out, best]
+
+    return run
+
+
+def test_two_host_threads_at_once():
+    """Each on a stream of its own, and then both on one; a refusal in one thread does not show in the other."""
+    import threading
+    runs = [_program(s) for s in (80, 81)]
+    want = [r() for r in runs]
+    torch.cuda.synchronize()
+    shared = torch.cuda.Stream()
+    bad = torch.zeros((3, 1), dtype=torch.int32, device=DEV), torch.zeros(3, dtype=torch.int32, device=DEV)
+    for own in (True, False):
+        got, wrong = [[], []], []
+
+        def work(i, stream):
+            try:
+                with torch.cuda.stream(stream):
+                    for n in range(20):
+                        got[i].append(runs[i]())
+                        if i == 1:
+                            with pytest.raises(mk.MkError, match="above 0"):
+                                mk.paged_attention(want[1][2][:3], want[1][0], want[1][1], *bad, scale=-1.0)
+            except BaseException as e:  # noqa: B902 (told by the test's thread)
+                wrong.append(e)
+
+        streams = [torch.cuda.Stream() if own else shared for _ in range(2)]
+        threads = [threading.Thread(target=work, args=(i, streams[i])) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not wrong, wrong
+        for i in range(2):
+            assert len(got[i]) == 20
+            for outs in got[i]:
+                assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_of_two_streams_that_meet(captured):
+    """The cache is filled on one stream, its two readers run on two, and the next call waits for both."""
+    run = _program(82)
+    want = run()
+    torch.cuda.synchronize()
+    split = torch.cuda.Stream()
+    if captured:
+        run(split)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run(split)
+        for _ in range(10):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    else:
+        for _ in range(30):
+            got = run(split)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_every_call_repeats_itself():
+    """The same bits from run to run, with the device empty or full of other work."""
+    run = _program(83)
+    want, other = run(), torch.cuda.Stream()
+    a = torch.randn((4096, 4096), device=DEV, dtype=BF)
+    for i in range(20):
+        if i % 2:
+            with torch.cuda.stream(other):
+                for _ in range(4):
+                    a @ a
+        flush()
+        got = run()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    torch.cuda.synchronize()
