@@ -296,3 +296,40 @@ def test_every_call_repeats_itself():
         got = run()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     torch.cuda.synchronize()
+
+
+def test_first_calls_of_a_process_are_captured():
+    """No call before the capture has loaded a kernel, asked for shared memory or made a tensor map."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import event_tensor_task_b200 as mk
+from test_gpu_serve import i32, cu
+d = "cuda:0"
+for dim, dtype in ((64, torch.bfloat16), (128, torch.float16)):
+    k, v = torch.randn((2, 200, 2, 16, dim), device=d).to(dtype)
+    x = torch.randn((6, 8, dim), device=d).to(dtype)
+    table = torch.arange(198, dtype=torch.int32, device=d).view(2, 99)
+    ctx, lens, bounds = i32([1500, 3]).to(d), i32([1505, 4]).to(d), cu([5, 1]).to(d)
+    logits = torch.randn((2, 5000), device=d).to(dtype)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q = mk.append_kv(x[:, :4], x[:, 4:6], x[:, 6:], k, v, table, ctx, bounds)
+        a = mk.prompt_attention(q, k, v, bounds, page_table=table, kv_lens=lens)
+        b = mk.paged_attention(q[4:], k, v, table, lens)
+        out = mk.process_logits(logits)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = mk.prompt_attention(q, k, v, bounds, page_table=table, kv_lens=lens), mk.paged_attention(q[4:], k, v, table, lens)
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    assert torch.equal(out[1], logits.float().argmax(-1).int())
+print("captured")
+""" % (os.path.dirname(here), here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
