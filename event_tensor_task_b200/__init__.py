@@ -397,10 +397,12 @@ def append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_
     q [T][Hq][D] (or None), k and v [T][Hkv][D] are the packed rows of all sequences (views of one projection's
     output do), ``cu_seqlens`` int32 [B + 1] their bounds and ``ctx_lens`` int32 [B] the tokens already cached.
     ``k_pages``/``v_pages`` are [n_pages][Hkv][page_size][D] in any order of the first three dimensions, ``page_table``
-    int32 [B][width]; one layer of a DenseDecoder's cache is such a pool, its slot ids [B][1] the table.
+    int32 [B][width]; one layer of a DenseDecoder's cache is such a pool, its slot ids [B][1] the table.  (A cache that
+    prompt_attention is to read takes pages of 16, 32, 64 or at least 128 rows.)
     ``rope_theta`` 0 (or None) stores the rows unturned.  Returns the turned queries: ``q_out`` (``q`` itself is
-    allowed), or a new tensor, whose rows behind the last sequence are not written.  ``status``: int32 [1],
-    see include/mk.h.  Like all calls here it runs on ``stream`` (default: torch's current one), asynchronously, and
+    allowed), or a new tensor, whose rows behind the last sequence are not written.  ``status``: int32 [1], cleared by
+    the caller, becomes an error code where a length or page id was out of bounds or a wait ran out (include/mk.h);
+    without one there is no sign of either.  Like all calls here it runs on ``stream`` (default: torch's current one), asynchronously, and
     carries no gradient."""
     return _tensors().append_kv(q, k, v, k_pages, v_pages, page_table, ctx_lens, cu_seqlens, rope_theta, q_out, status,
                                 stream)
@@ -411,8 +413,8 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, page_table=None, kv_lens=None, ca
     """Attention over whole prompts, packed one after the other (mk_prompt_attention).
 
     q [T][Hq][D]; sequence b's queries are rows cu_q[b] .. cu_q[b + 1].  Without ``page_table``, k and v are
-    [Tk][Hkv][D] with bounds ``cu_k`` (default ``cu_q``); with it they are cache pages as in :func:`append_kv` and
-    ``kv_lens`` int32 [B] counts each sequence's keys, the new tokens' own among them.  Causal: the last query of a
+    [Tk][Hkv][D] with bounds ``cu_k`` (default ``cu_q``); with it they are cache pages as in :func:`append_kv`, of 16,
+    32, 64 or at least 128 rows, and ``kv_lens`` int32 [B] counts each sequence's keys, the new tokens' own among them.  Causal: the last query of a
     sequence sees all its keys, each one before it one less.  ``scale`` defaults to 1 / sqrt(D).  Returns ``out``, or
     a new tensor, whose rows behind the last sequence are not written.  ``workspace``: uint8,
     mk_prompt_attention_workspace_bytes long, not to be shared by calls that overlap; by default one is allocated where

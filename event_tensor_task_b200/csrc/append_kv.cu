@@ -11,8 +11,9 @@
 //
 // Bound: memory.  Every row is read and written once, 16 bytes a thread and
 // access; a thread turns 8 pairs (a 16-byte piece of each half of a head).
-// Measured (one B200, in a graph): 8,148 tokens of 32/8 heads of 128 (200 MB)
-// in 39 us, 5.1 TB/s; 64 tokens of 64 sequences in 3.8 us.
+// Measured (one B200, in a graph, inputs that are not in L2): 8,148 tokens of
+// 32/8 heads of 128 (200 MB) in 39 us, 5.1 TB/s; 64 tokens of 64 sequences in
+// 3.3 us.
 #include <cmath>
 
 #include "serve.cuh"

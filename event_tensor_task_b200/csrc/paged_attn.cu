@@ -21,10 +21,11 @@
 //    tensor pipe is nearly idle either way.  With G <= 8 the spare rows carry
 //    what rounding takes off the probabilities (value and remainder), above 8
 //    the remainders take a second MMA: the sum sees ~16 bits of p.
-// Measured (one B200, in a graph): 475 MB of keys and values in 86 us, 78 of
-// them the first kernel (6.1 TB/s); 286 MB of 32 sequences in 54 us; one
-// sequence of 1,025 keys, 32/8 heads, in 6.6 us.  About 8 us of a call are
-// launch, search, the first round trips and the join, whatever its size.
+// Measured (one B200, calls one after the other on inputs that are not in L2):
+// 475 MB of keys and values in 90 us, 5.3 TB/s (the first kernel alone, under
+// the profiler, 85); 286 MB of 32 sequences in 57 us; one sequence of 1,025
+// keys, 32/8 heads, in 7 us.  About 8 us of a call are launch, search, the
+// first round trips and the join, whatever its size.
 #include <algorithm>
 #include <cmath>
 

@@ -4,10 +4,14 @@
 // Mathematics: out_i = sum_j p_ij v_j / sum_j p_ij, p_ij = 2^(c (q_i.k_j) - m_i),
 // c = scale log2 e, in one pass over the keys with a running reference m_i.
 // m_i follows the running maximum only when that has grown by more than 8 in
-// the exponent: the probabilities then stay below 2^8, exact in the same way,
-// and the accumulated output is rescaled a few times a row instead of at every
-// tile.  P is rounded to the type for its product, as the tensor cores take it;
-// its sum is that of the unrounded values in fp32.
+// the exponent (a published idea for attention on this GPU): the probabilities
+// then stay below 2^8, exact in the same way, and the accumulated output is
+// rescaled a few times a row instead of at every tile.  P is rounded to the
+// type for its product, as the tensor cores take it; its sum is that of the
+// unrounded values in fp32.  A remainder of P beside it, as single tokens have
+// it, would be half as many MMAs again and is left out: the error is 1.25 times
+// that of a form rounded once at the end (bf16 2.0e-3 against 1.6e-3, fp16
+// 2.5e-4 against 2.0e-4, root mean square).
 //
 // Rows: the G = n_q_heads / n_kv_heads query heads that share a kv head are
 // stacked, so a tile of 128 rows is floor(128 / G) tokens times G heads (one
@@ -31,10 +35,16 @@
 //
 // Bound: per tile of 128 x 128 scores the exponentials take 1,024 cycles of the
 // MUFU, the products 1,024 of the tensor pipe at D = 128 and 512 at D = 64.
-// Measured: a tile takes about 1,600 cycles at D = 128 (1,280 TFLOP/s at full
-// clock, 16k tokens, 32 heads; the power limit takes it to 1,130 when repeated)
-// and 1,350 at D = 64: a row's chain (S ready, maximum, exponentials, P, the
-// product's wait) and its ~600 instructions on two softmax warps a scheduler.
+// Measured (one B200; packed causal prompts of 64 to 4,096 tokens, 32/8 heads):
+// a block takes 1.58 us a tile at D = 64 (two blocks an SM) and 1.75 us a pair
+// of tiles at D = 128, that is 1,350 and 1,500 cycles a tile: a row's chain (S
+// ready, maximum, exponentials, P, the product's wait) and its ~600
+// instructions on two softmax warps a scheduler.  A piece of work's way in and
+// out takes 4.0 and 5.0 us more: its first loads and scores, O to memory by
+// the warps that would be in the next softmax.  16k tokens, 32 heads of 128:
+// 1.75 ms for a call alone (1,260 TFLOP/s), 1.94 to 2.0 when repeated (1,100
+// to 1,130, the power limit).  The instances spill 68 bytes (D = 64) and 16
+// (D = 128) of a thread's registers.
 // Tried and slower: two threads a row (2.13 against 1.80 ms on 16k tokens), an
 // eighth to a half of the exponentials as a polynomial on the FMA pipes (equal
 // at an eighth, 10 % slower at 3/8), two tiles a block at D = 64 (222 against
@@ -53,7 +63,7 @@ constexpr int kTiles64 = 1;      // row tiles of a block at D = 64
 constexpr int kParts = 2;        // halves of a P tile, handed to the MMAs one by one
 constexpr int kShares = 2;       // of the work for each resident block (see find_cut)
 constexpr int kMostPieces = 64;  // of a block's keys
-constexpr int kLeastTiles = 6;   // key tiles of a piece: a block's way in and out costs about two
+constexpr int kLeastTiles = 6;   // key tiles of a piece: a block's way in and out costs two to three
 constexpr float kSlack = 8.f;    // log2 growth of the maximum that is left to the probabilities
 constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait
 

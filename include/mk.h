@@ -437,9 +437,11 @@ void mk_plan_destroy(mk_plan* p);
  *    page id outside [0, n_pages), a length below zero or beyond what the
  *    page table or the rows hold is never followed.  The rows concerned are
  *    skipped (append) or see only the keys that are there (attention; a bad
- *    page reads as zeros), and *status, where given, becomes
- *    MK_ERR_DEVICE_BOUNDS.  The status word is written only then: the caller
- *    clears it;
+ *    page reads as zeros; a pool without pages holds no keys), and *status,
+ *    where given, becomes MK_ERR_DEVICE_BOUNDS.  A wait inside a kernel that
+ *    takes more than 2 s ends its block's work, rows may stay unwritten, and
+ *    *status becomes MK_ERR_DEVICE_TIMEOUT.  The status word is written only
+ *    then: the caller clears it.  Without one such a call gives no sign;
  *  - MK_ERR_INVALID_ARG for null or misaligned pointers and sizes out of
  *    range, MK_ERR_UNSUPPORTED for a valid request that is not implemented.
  *    A call with nothing to do (no rows) returns MK_OK and launches nothing.
@@ -454,7 +456,8 @@ void mk_plan_destroy(mk_plan* p);
  * of sequence b is row t % page_size of page page_table[b][t / page_size].
  * One layer of a decode plan's slot cache ([n_slots][n_kv_heads][max_ctx]
  * [head_dim]) is a pool with one page of max_ctx rows per slot; its page table
- * is the slot ids, one column. */
+ * is the slot ids, one column (mk_prompt_attention then wants a max_ctx of 16,
+ * 32, 64 or at least 128). */
 typedef struct mk_kv_pages {
   void* k;                /* post-RoPE keys */
   void* v;
